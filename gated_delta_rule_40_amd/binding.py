@@ -21,7 +21,9 @@ GDR_OK = 0
 
 LIB_PATH = Path(__file__).resolve().parent / "libgdr.so"
 EXPORTED = ("gdr_decode_step", "gdr_prefill_workspace_size", "gdr_prefill_chunked",
-            "gdr_prefill_chunked_noalloc", "gdr_strerror")
+            "gdr_prefill_chunked_noalloc", "gdr_conv_step", "gdr_conv_prefill", "gdr_ssm_step",
+            "gdr_ssm_workspace_size", "gdr_ssm_prefill", "gdr_kv_append",
+            "gdr_attn_workspace_size", "gdr_attn_cached", "gdr_strerror")
 NOALLOC_SCRATCH_BYTES = 128 << 20   # GDR_NOALLOC_SCRATCH_BYTES
 
 
@@ -33,6 +35,19 @@ class GdrError(RuntimeError):
 
 class gdr_dims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "H_qk", "H_v", "dk", "dv", "chunk")]
+
+
+class gdr_conv_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "W", "c0", "c1", "c2")]
+
+
+class gdr_ssm_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "G", "H", "N", "P")]
+
+
+class gdr_kv_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32)
+                for n in ("B", "T", "H_q", "H_kv", "D", "page", "n_pages", "max_pages")]
 
 
 _lib = None
@@ -60,6 +75,20 @@ def load_library(path: Path | str | None = None):
     lib.gdr_prefill_chunked_noalloc.argtypes = [dims_p, i32, i32, vp, vp, vp, fp, fp, fp, fp, fp,
                                                 fp, vp, ctypes.c_float, i32, vp]
     lib.gdr_prefill_chunked_noalloc.restype = i32
+    size, i64, f32 = ctypes.c_size_t, ctypes.c_int64, ctypes.c_float
+    conv_p, ssm_p, kv_p = (ctypes.POINTER(t) for t in (gdr_conv_dims, gdr_ssm_dims, gdr_kv_dims))
+    lib.gdr_conv_step.argtypes = [conv_p, i32, i32, vp, i64, vp, vp, vp, vp, vp]
+    lib.gdr_conv_prefill.argtypes = [conv_p, i32, i32, vp, i64] + [vp] * 9
+    lib.gdr_ssm_step.argtypes = [ssm_p, i32] + [vp] * 8
+    lib.gdr_ssm_workspace_size.argtypes = [ssm_p, i32]
+    lib.gdr_ssm_prefill.argtypes = [ssm_p, i32] + [vp] * 12 + [size, vp]
+    lib.gdr_kv_append.argtypes = [kv_p, i32] + [vp] * 10
+    lib.gdr_attn_workspace_size.argtypes = [kv_p, i32]
+    lib.gdr_attn_cached.argtypes = [kv_p, i32] + [vp] * 9 + [f32, vp, size, vp]
+    for name in ("gdr_conv_step", "gdr_conv_prefill", "gdr_ssm_step", "gdr_ssm_prefill",
+                 "gdr_kv_append", "gdr_attn_cached"):
+        getattr(lib, name).restype = i32
+    lib.gdr_ssm_workspace_size.restype = lib.gdr_attn_workspace_size.restype = size
     lib.gdr_strerror.argtypes = [i32]
     lib.gdr_strerror.restype = ctypes.c_char_p
     if path is None:
@@ -201,3 +230,210 @@ def gdr_prefill_chunked_noalloc(q, k, v, gate_in, beta_logit, state_in, state_ou
                                          _stream(q.device, stream))
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_prefill_chunked_noalloc")
+
+
+# ---------------------------------------------------------------------------
+# The layers beside the gated delta rule.  Sizes are read from the tensors; the
+# launch goes to the tensors' device whatever the current one is.
+# ---------------------------------------------------------------------------
+_F8 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _ptr(t, name, shape, dtype, device):
+    """Device address of a dense tensor of exactly this shape, dtype and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, name, shape, dtype, device):
+    return None if t is None else _ptr(t, name, shape, dtype, device)
+
+
+def _lead(t, name, dims):
+    """Shape, dtype and device of the tensor that sets the sizes of a call."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}, expected a GPU")
+    return t.shape, _io_code(t.dtype), t.device
+
+
+def _launch(name, dev, stream, *args):
+    """Calls an entry point with the stream as its last argument, on `dev`."""
+    fn = getattr(load_library(), name)
+    here = torch.cuda.current_device()
+    if dev.index != here:
+        torch.cuda.set_device(dev)
+    try:
+        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        rc = fn(*args, s.cuda_stream)
+    finally:
+        if dev.index != here:
+            torch.cuda.set_device(here)
+    if rc != GDR_OK:
+        raise GdrError(rc, name)
+
+
+def gdr_conv_step(x, weight, bias, state, y, *, silu=True, stream=None):
+    """One token of the short causal convolution.  x [B,C] (float32 or bfloat16;
+    its rows may lie apart, as in a slice of a wider row), weight [C,W] fp32,
+    bias [C] fp32 or None, state [B,W-1,C] in x's dtype (oldest input first,
+    updated in place), y [B,C]."""
+    (B, C), io, dev = _lead(x, "x", 2)
+    W = weight.shape[-1]
+    row = C if B <= 1 and x.is_contiguous() else x.stride(0)
+    if x.stride(1) != 1 and C > 1:
+        raise ValueError("x's channels must be contiguous")
+    f32 = torch.float32
+    _launch("gdr_conv_step", dev, stream, gdr_conv_dims(B, 1, W, C, 0, 0), io, int(bool(silu)),
+            x.data_ptr(), row, _ptr(weight, "weight", (C, W), f32, dev),
+            _opt(bias, "bias", (C,), f32, dev), _ptr(state, "state", (B, W - 1, C), x.dtype, dev),
+            _ptr(y, "y", (B, C), x.dtype, dev))
+
+
+def gdr_conv_prefill(x, weight, bias, state_in, state_out, outs, *, silu=True, lens=None,
+                     stream=None):
+    """The short causal convolution over T tokens.  x [B,T,C] (tokens may lie
+    apart, evenly over the whole batch), weight [C,W], bias [C] or None,
+    state_in (or None) and state_out [B,W-1,C], outs one to three tensors
+    [B,T,c] whose widths add up to C, lens [B] int32 or None."""
+    (B, T, C), io, dev = _lead(x, "x", 3)
+    W = weight.shape[-1]
+    if x.is_contiguous():
+        row = C
+    else:
+        row = x.stride(1)
+        if x.stride(2) != 1 or (B > 1 and x.stride(0) != T * row):
+            raise ValueError("x must be rows of contiguous channels, evenly apart")
+    if not 1 <= len(outs) <= 3:
+        raise ValueError(f"one to three outputs, got {len(outs)}")
+    c = [o.shape[-1] for o in outs]
+    if sum(c) != C or 0 in c:
+        raise ValueError(f"outputs of widths {c} do not split {C} channels")
+    ys = [_ptr(o, f"outs[{i}]", (B, T, c[i]), x.dtype, dev) for i, o in enumerate(outs)]
+    c += [0] * (3 - len(c))
+    ys += [None] * (3 - len(ys))
+    f32, st = torch.float32, (B, W - 1, C)
+    _launch("gdr_conv_prefill", dev, stream, gdr_conv_dims(B, T, W, *c), io, int(bool(silu)),
+            x.data_ptr(), row, _ptr(weight, "weight", (C, W), f32, dev),
+            _opt(bias, "bias", (C,), f32, dev), _opt(lens, "lens", (B,), torch.int32, dev),
+            _opt(state_in, "state_in", st, x.dtype, dev),
+            _ptr(state_out, "state_out", st, x.dtype, dev), *ys)
+
+
+def gdr_ssm_step(xbc, dt, A_log, dt_bias, D, state, y, *, G, H, N, P, stream=None):
+    """One token of the selective state space scan.  xbc [B, H*P + 2*G*N]
+    (float32 or bfloat16), dt [B,H] fp32, A_log [H], dt_bias and D [H] or None,
+    state [B,H,N,P] fp32 (updated in place), y [B,H,P] in xbc's dtype."""
+    (B, width), io, dev = _lead(xbc, "xbc", 2)
+    f32 = torch.float32
+    _launch("gdr_ssm_step", dev, stream, gdr_ssm_dims(B, 1, G, H, N, P), io,
+            _ptr(xbc, "xbc", (B, H * P + 2 * G * N), xbc.dtype, dev),
+            _ptr(dt, "dt", (B, H), f32, dev), _ptr(A_log, "A_log", (H,), f32, dev),
+            _opt(dt_bias, "dt_bias", (H,), f32, dev), _opt(D, "D", (H,), f32, dev),
+            _ptr(state, "state", (B, H, N, P), f32, dev), _ptr(y, "y", (B, H, P), xbc.dtype, dev))
+
+
+def gdr_ssm_workspace_size(B, T, G, H, N, P, io_dtype) -> int:
+    return int(load_library().gdr_ssm_workspace_size(gdr_ssm_dims(B, T, G, H, N, P),
+                                                     _io_code(io_dtype)))
+
+
+def _space(workspace, dev):
+    if workspace is None:
+        return None, 0
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the same device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def gdr_ssm_prefill(x, b, c, dt, A_log, dt_bias, D, state_in, state_out, y, workspace, *,
+                    G, H, N, P, lens=None, stream=None):
+    """The selective state space scan over T tokens.  x [B,T,H,P], b and c
+    [B,T,G,N] (float32 or bfloat16; dense, the last two dimensions may come as
+    one), dt [B,T,H] fp32, A_log [H], dt_bias and D [H] or None, state_in (or
+    None) and state_out [B,H,N,P] fp32, y like x, workspace a uint8 tensor of
+    at least gdr_ssm_workspace_size() bytes (None if that is 0), lens [B] int32
+    or None."""
+    if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
+        raise ValueError("x must be a tensor [B,T,H,P] or [B,T,H*P]")
+    shape, io, dev = _lead(x, "x", x.dim())
+    B, T = shape[:2]
+
+    def rows(t, name, heads, width):
+        flat = isinstance(t, torch.Tensor) and t.dim() == 3
+        return _ptr(t, name, (B, T, heads * width) if flat else (B, T, heads, width), x.dtype, dev)
+
+    f32, st = torch.float32, (B, H, N, P)
+    ws, ws_bytes = _space(workspace, dev)
+    _launch("gdr_ssm_prefill", dev, stream, gdr_ssm_dims(B, T, G, H, N, P), io,
+            rows(x, "x", H, P), rows(b, "b", G, N), rows(c, "c", G, N),
+            _ptr(dt, "dt", (B, T, H), f32, dev), _ptr(A_log, "A_log", (H,), f32, dev),
+            _opt(dt_bias, "dt_bias", (H,), f32, dev), _opt(D, "D", (H,), f32, dev),
+            _opt(lens, "lens", (B,), torch.int32, dev), _opt(state_in, "state_in", st, f32, dev),
+            _ptr(state_out, "state_out", st, f32, dev), rows(y, "y", H, P), ws, ws_bytes)
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table, pos, lens, B, H_kv, D, dev):
+    """Pool sizes and addresses of the cache's tensors."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a tensor [n_pages,H_kv,page,D]")
+    if k_cache.dtype not in _F8:
+        raise ValueError(f"k_cache has dtype {k_cache.dtype}, expected float8_e4m3fn or uint8")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor [B,max_pages]")
+    n_pages, page, per = k_cache.shape[0], k_cache.shape[2], block_table.shape[1]
+    f8, f32, i32 = k_cache.dtype, torch.float32, torch.int32
+    return (page, n_pages, per), (
+        _ptr(k_cache, "k_cache", (n_pages, H_kv, page, D), f8, dev),
+        _ptr(v_cache, "v_cache", (n_pages, H_kv, D, page), f8, dev),
+        _ptr(k_scale, "k_scale", (n_pages, H_kv), f32, dev),
+        _ptr(v_scale, "v_scale", (n_pages, H_kv), f32, dev),
+        _ptr(block_table, "block_table", (B, per), i32, dev), _ptr(pos, "pos", (B,), i32, dev),
+        _opt(lens, "lens", (B,), i32, dev))
+
+
+def gdr_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, pos, *, lens=None,
+                  stream=None):
+    """Writes new tokens' keys and values, k and v [B,T,H_kv,D] (float32 or
+    bfloat16), into their pages: k_cache [n_pages,H_kv,page,D] and v_cache
+    [n_pages,H_kv,D,page] (float8_e4m3fn or uint8), k_scale and v_scale
+    [n_pages,H_kv] fp32, block_table [B,max_pages], pos and lens [B] int32."""
+    (B, T, H_kv, D), io, dev = _lead(k, "k", 4)
+    sizes, (kc, vc, ks, vs, bt, ps, ln) = _cache_args(k_cache, v_cache, k_scale, v_scale,
+                                                      block_table, pos, lens, B, H_kv, D, dev)
+    _launch("gdr_kv_append", dev, stream, gdr_kv_dims(B, T, 0, H_kv, D, *sizes), io,
+            _ptr(k, "k", (B, T, H_kv, D), k.dtype, dev), _ptr(v, "v", (B, T, H_kv, D), k.dtype, dev),
+            bt, ps, ln, kc, vc, ks, vs)
+
+
+def gdr_attn_workspace_size(B, T, H_q, H_kv, D, page, max_pages, io_dtype) -> int:
+    return int(load_library().gdr_attn_workspace_size(
+        gdr_kv_dims(B, T, H_q, H_kv, D, page, 0, max_pages), _io_code(io_dtype)))
+
+
+def gdr_attn_cached(q, k_cache, v_cache, k_scale, v_scale, block_table, pos, o, workspace=None, *,
+                    scale, lens=None, stream=None):
+    """Attention of T new tokens per row over the cache.  q and o [B,T,H_q,D]
+    (float32 or bfloat16); the cache, block_table, pos and lens as in
+    gdr_kv_append, with the new tokens already written; workspace a uint8
+    tensor of at least gdr_attn_workspace_size() bytes (None if that is 0)."""
+    (B, T, H_q, D), io, dev = _lead(q, "q", 4)
+    H_kv = k_cache.shape[1]
+    sizes, (kc, vc, ks, vs, bt, ps, ln) = _cache_args(k_cache, v_cache, k_scale, v_scale,
+                                                      block_table, pos, lens, B, H_kv, D, dev)
+    ws, ws_bytes = _space(workspace, dev)
+    _launch("gdr_attn_cached", dev, stream, gdr_kv_dims(B, T, H_q, H_kv, D, *sizes), io,
+            _ptr(q, "q", (B, T, H_q, D), q.dtype, dev), kc, vc, ks, vs, bt, ps, ln,
+            _ptr(o, "o", (B, T, H_q, D), q.dtype, dev), float(scale), ws, ws_bytes)

@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include "api_check.hpp"
 #include "gdr.h"
 #include "gdr_internal.h"
 
@@ -13,27 +14,10 @@ static_assert(GDR_NOALLOC_SCRATCH_BYTES == gdr::kNoallocScratchBytes,
 
 namespace {
 
+using namespace gdr::check;
+
 bool supported_head_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool supported_chunk(int c) { return c == 16 || c == 32 || c == 64; }
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, size_t bytes) {
-  uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Range{lo, lo + bytes};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-
-bool overlaps_any(Range a, const Range* others, int n) {
-  for (int i = 0; i < n; ++i)
-    if (overlap(a, others[i])) return true;
-  return false;
-}
 
 int check_sizes(const gdr_dims* d, gdr_dtype io, gdr_gate gate, bool prefill) {
   if (!d) return GDR_E_NULL;
@@ -179,10 +163,10 @@ const char* gdr_strerror(int status) {
   switch (status) {
     case GDR_OK: return "ok";
     case GDR_E_NULL: return "a required pointer is NULL";
-    case GDR_E_SHAPE: return "invalid shape (negative size, H_v not a multiple of H_qk, or too large)";
-    case GDR_E_DTYPE: return "unknown io dtype or gate kind";
-    case GDR_E_UNSUPPORTED: return "dk/dv must be 16, 32, 64 or 128 and chunk 16, 32 or 64";
-    case GDR_E_WORKSPACE: return "workspace is NULL or smaller than gdr_prefill_workspace_size()";
+    case GDR_E_SHAPE: return "invalid shape (negative size, heads not a multiple of their groups, or too large)";
+    case GDR_E_DTYPE: return "unknown io dtype, gate kind or activation";
+    case GDR_E_UNSUPPORTED: return "a head width, chunk, convolution width or page size is outside the compiled set";
+    case GDR_E_WORKSPACE: return "workspace is NULL or smaller than the entry point's size query";
     case GDR_E_HIP: return "HIP runtime error at kernel launch";
     case GDR_E_ALIAS: return "an output, the state or the workspace overlaps a buffer it must not";
     case GDR_E_ALIGN: return "tensor pointer is not 16-byte aligned";

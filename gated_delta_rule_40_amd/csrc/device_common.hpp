@@ -140,4 +140,14 @@ __device__ __forceinline__ float fused_log_decay(float x, float A_log, float dt_
   return -expf(A_log) * softplusf(x + dt_bias);
 }
 
+// e^x and x sigmoid(x) through the hardware's exp2 and reciprocal (about one
+// unit in the last place each): where a value takes a handful of
+// multiply-adds, the library forms would cost more than all the rest.
+__device__ __forceinline__ float exp_hw(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
+}
+__device__ __forceinline__ float silu_hw(float x) {
+  return x * __builtin_amdgcn_rcpf(1.0f + exp_hw(-x));
+}
+
 }  // namespace gdr

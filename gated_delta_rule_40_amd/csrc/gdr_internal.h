@@ -74,4 +74,71 @@ int recurrent_dv_slice(int B, int H_v, int dv);
 size_t recurrent_lds_bytes(int T, int dk, int dv_slice);
 hipError_t launch_recurrent(const PrefillArgs& a, int io_bf16, hipStream_t stream);
 
+// Argument block of the short convolution (step: T = 1, y0 takes all channels).
+struct ConvArgs {
+  const void* x;        // rows of C channels, x_stride elements apart
+  const float* weight;  // [C,W]
+  const float* bias;    // [C] or nullptr
+  const int* lens;      // [B] or nullptr
+  const void* state_in;   // [B,W-1,C] or nullptr
+  void* state_out;      // [B,W-1,C]
+  void* y[3];
+  long long x_stride;
+  int B, T, W, C;
+  int c[3];             // widths of the outputs
+  int silu;
+};
+hipError_t launch_conv(const ConvArgs& a, int io_bf16, hipStream_t stream);
+// Workgroups launch_conv starts for these sizes on the narrow (one channel a
+// thread) path, the larger of its two.
+long long conv_max_grid(int B, int T, int C);
+
+// Argument block of the selective state space scan.
+struct SsmArgs {
+  const void* x;          // step: packed x|B|C rows; prefill [B,T,H,P]
+  const void* b;          // [B,T,G,N] (prefill)
+  const void* c;          // [B,T,G,N] (prefill)
+  const float* dt;        // [B,T,H]
+  const float* A_log;     // [H]
+  const float* dt_bias;   // [H] or nullptr
+  const float* D;         // [H] or nullptr
+  const int* lens;        // [B] or nullptr
+  const float* state_in;  // [B,H,N,P] or nullptr
+  float* state_out;       // [B,H,N,P]
+  void* y;                // [B,T,H,P]
+  void* ws;
+  int B, T, G, H, N, P;
+};
+hipError_t launch_ssm_step(const SsmArgs& a, int io_bf16, hipStream_t stream);
+size_t ssm_workspace_bytes(int B, int T, int G, int H, int N, int P, int io_bf16);
+hipError_t launch_ssm_prefill(const SsmArgs& a, int io_bf16, hipStream_t stream);
+
+// Argument blocks of the 8-bit cache.
+struct KvArgs {
+  const void* k;  // [B,T,H_kv,D] new keys and values (append)
+  const void* v;
+  const void* q;  // [B,T,H_q,D] (attention)
+  void* o;
+  const int* block_table;  // [B,max_pages]
+  const int* pos;          // [B]
+  const int* lens;         // [B] or nullptr
+  uint8_t* k_cache;        // [n_pages,H_kv,page,D] e4m3 codes
+  uint8_t* v_cache;        // [n_pages,H_kv,D,page]
+  float* k_scale;          // [n_pages,H_kv]
+  float* v_scale;
+  void* ws;
+  int B, T, H_q, H_kv, D, page, n_pages, max_pages;
+  float scale;
+};
+hipError_t launch_kv_append(const KvArgs& a, int io_bf16, hipStream_t stream);
+// Pages that T consecutive positions can touch at most.
+inline long long kv_touched_pages(int T, int page) {
+  return (static_cast<long long>(T) + page - 2) / page + 1;
+}
+size_t attn_workspace_bytes(const KvArgs& a, int io_bf16);
+hipError_t launch_attn(const KvArgs& a, int io_bf16, hipStream_t stream);
+
+// Workgroups a launch may have: 256 threads each within 32 bits of threads.
+constexpr long long kMaxGrid = (1ll << 24) - 1;
+
 }  // namespace gdr

@@ -82,9 +82,9 @@ typedef struct gdr_dims {
 typedef enum gdr_status {
   GDR_OK = 0,
   GDR_E_NULL = -1,        /* a required pointer is NULL                         */
-  GDR_E_SHAPE = -2,       /* negative size, H_v % H_qk != 0, ...                */
-  GDR_E_DTYPE = -3,       /* unknown io dtype or gate kind                      */
-  GDR_E_UNSUPPORTED = -4, /* dk/dv/chunk outside the compiled set               */
+  GDR_E_SHAPE = -2,       /* negative size, H_v % H_qk != 0, H % G != 0, ...    */
+  GDR_E_DTYPE = -3,       /* unknown io dtype, gate kind or activation          */
+  GDR_E_UNSUPPORTED = -4, /* dk/dv/chunk/W/N/P/D/page outside the compiled set  */
   GDR_E_WORKSPACE = -5,   /* workspace NULL or smaller than the size query      */
   GDR_E_HIP = -6,         /* the HIP runtime reported an error at launch        */
   GDR_E_ALIAS = -7,       /* o, the state or the workspace overlaps a buffer    */
@@ -213,6 +213,201 @@ int gdr_prefill_chunked_noalloc(const gdr_dims* dims, gdr_dtype io, gdr_gate gat
                                 const float* gate_in, const float* A_log, const float* dt_bias,
                                 const float* beta_logit, const float* state_in, float* state_out,
                                 void* o, float scale, int l2norm_qk, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The layers beside the gated delta rule: the short causal convolution that a
+ * recurrent layer's input row passes first, the selective state space scan,
+ * and attention over a cache of 8-bit keys and values.  The conventions at
+ * the top of this file hold; what differs is stated at each function.
+ *
+ * Padded batches: where a function takes `lens` ([B] int32 in device memory,
+ * NULL for T tokens in every row), row b holds lens[b] tokens (taken as 0 if
+ * negative, as T if larger).  Tokens behind them are not read, and their
+ * output rows are left as they were.
+ * ------------------------------------------------------------------------ */
+
+/* Sizes of the short convolution: W taps over c0 + c1 + c2 channels, written
+ * as one to three dense outputs (c1 = c2 = 0 for one, c2 = 0 for two). */
+typedef struct gdr_conv_dims {
+  int32_t B, T, W, c0, c1, c2;
+} gdr_conv_dims;
+
+typedef enum gdr_act { GDR_ACT_NONE = 0, GDR_ACT_SILU = 1 } gdr_act;
+
+/*
+ * gdr_conv_step -- one token of a short causal convolution per channel:
+ *
+ *     y[c] = act(bias[c] + sum_w weight[c][w] * u[w][c])
+ *
+ * where u is the row's last W inputs, oldest first: the state, then x.  The
+ * state then drops its oldest row and takes x.  With C = 2*H_qk*dk + H_v*dv
+ * the output is the packed row of gdr_decode_step, with C = H*P + 2*G*N that
+ * of gdr_ssm_step.
+ *
+ *   dims      B, W (2, 3 or 4), C = c0 + c1 + c2 channels (T ignored; the
+ *             output is one row of C channels however they are given)
+ *   x         [B] rows of C channels, io dtype, x_stride elements apart
+ *             (x_stride >= C); aligned to its element.  Rows and outputs that
+ *             are 16-byte aligned throughout take the wide path.
+ *   weight    [C,W] fp32, 16-byte aligned; weight[c][W-1] multiplies x
+ *   bias      [C] fp32 or NULL
+ *   state     [B,W-1,C] io dtype, oldest input first, updated IN PLACE; must
+ *             not overlap x, weight or bias
+ *   y         [B,C] io dtype, must not overlap the state or an input
+ */
+int gdr_conv_step(const gdr_conv_dims* dims, gdr_dtype io, gdr_act act, const void* x,
+                  int64_t x_stride, const float* weight, const float* bias, void* state, void* y,
+                  hipStream_t stream);
+
+/*
+ * gdr_conv_prefill -- gdr_conv_step for T tokens per row, with the channels
+ * split over up to three outputs: c0 | c1 | c2 become the dense q | k | v of
+ * gdr_prefill_chunked or the x | b | c of gdr_ssm_prefill.
+ *
+ *   x          [B,T] rows of C channels, x_stride elements apart
+ *   lens       [B] int32 or NULL
+ *   state_in   [B,W-1,C] io dtype, the inputs before the first token, oldest
+ *              first, or NULL for zeros
+ *   state_out  [B,W-1,C] io dtype, the last W-1 inputs (those of state_in
+ *              count); may be state_in itself, else must not overlap it, nor
+ *              x, weight or bias
+ *   y0, y1, y2 [B,T,c0], [B,T,c1], [B,T,c2] io dtype (ignored where the width
+ *              is 0), no two overlapping, nor any input or state
+ *   T == 0     copies state_in to state_out (zeros when it is NULL)
+ */
+int gdr_conv_prefill(const gdr_conv_dims* dims, gdr_dtype io, gdr_act act, const void* x,
+                     int64_t x_stride, const float* weight, const float* bias,
+                     const int32_t* lens, const void* state_in, void* state_out, void* y0,
+                     void* y1, void* y2, hipStream_t stream);
+
+/* Sizes of the selective state space scan: H heads of width P with a state of
+ * N rows each, in G groups of H / G neighbouring heads that share B and C.
+ * N and P in {16, 32, 64, 128}.  A step ignores T. */
+typedef struct gdr_ssm_dims {
+  int32_t B, T, G, H, N, P;
+} gdr_ssm_dims;
+
+/*
+ * gdr_ssm_step -- one token of the selective state space scan.  Per batch row
+ * and head h of group g = h / (H / G), with input x (P), B and C (N):
+ *
+ *     d = softplus(dt + dt_bias[h])
+ *     S <- exp(-exp(A_log[h]) d) S + d B x^T
+ *     y  = S^T C + D[h] x
+ *
+ *   xbc      [B, H*P + 2*G*N] io dtype: x heads, then B groups, then C groups
+ *   dt       [B,H] fp32
+ *   A_log    [H] fp32
+ *   dt_bias  [H] fp32 or NULL (zeros)
+ *   D        [H] fp32 or NULL (zeros)
+ *   state    [B,H,N,P] fp32, updated IN PLACE; must not overlap an input
+ *   y        [B,H,P] io dtype; must not overlap the state or an input
+ */
+int gdr_ssm_step(const gdr_ssm_dims* dims, gdr_dtype io, const void* xbc, const float* dt,
+                 const float* A_log, const float* dt_bias, const float* D, float* state, void* y,
+                 hipStream_t stream);
+
+/* gdr_ssm_workspace_size -- bytes of device workspace gdr_ssm_prefill needs
+ * (may be 0); 0 as well for unsupported arguments. */
+size_t gdr_ssm_workspace_size(const gdr_ssm_dims* dims, gdr_dtype io);
+
+/*
+ * gdr_ssm_prefill -- T tokens of the scan; equals T steps up to rounding.
+ *
+ *   x          [B,T,H,P] io dtype
+ *   b, c       [B,T,G,N] io dtype
+ *   dt         [B,T,H] fp32
+ *   A_log, dt_bias, D   as in gdr_ssm_step
+ *   lens       [B] int32 or NULL
+ *   state_in   [B,H,N,P] fp32 or NULL for zeros
+ *   state_out  [B,H,N,P] fp32, the state behind the last token of each row;
+ *              may be state_in itself, else must not overlap it, nor any
+ *              other input
+ *   y          [B,T,H,P] io dtype; must not overlap any input or the state
+ *   workspace  gdr_ssm_workspace_size() bytes (NULL if that is 0), 16-byte
+ *              aligned, uninitialised, overlapping nothing else; one for each
+ *              call that may run at the same time
+ *   T == 0     copies state_in to state_out (zeros when it is NULL)
+ */
+int gdr_ssm_prefill(const gdr_ssm_dims* dims, gdr_dtype io, const void* x, const void* b,
+                    const void* c, const float* dt, const float* A_log, const float* dt_bias,
+                    const float* D, const int32_t* lens, const float* state_in, float* state_out,
+                    void* y, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The key/value cache is a pool of n_pages pages of `page` tokens.  A page
+ * holds e4m3 codes (OCP, 448 at most, no infinity) and one fp32 scale per
+ * head for its keys and one for its values; a code c stands for c * scale:
+ *
+ *     k_cache [n_pages,H_kv,page,D]    k_scale [n_pages,H_kv]
+ *     v_cache [n_pages,H_kv,D,page]    v_scale [n_pages,H_kv]
+ *
+ * Values are stored transposed: attention contracts over the tokens, and so
+ * reads them in the order in which the matrix instructions take them.  Scales
+ * are powers of two from 2^-100 up.
+ *
+ * block_table [B,max_pages] int32 names row b's pages in order: its position
+ * p lies in page block_table[b][p / page], slot p % page.  pos [B] int32 is
+ * the position of the row's first new token (what is cached before the call
+ * is [0, pos)).  Entries outside [0, n_pages) and positions outside the table
+ * (negative ones, or past max_pages * page) are not followed: such tokens are
+ * not written, and attention takes them as absent.  A pool or table without
+ * pages may be NULL.
+ *
+ * H_q a multiple of H_kv; D in {64, 128}; page in {16, 32, 64, 128}.
+ * gdr_kv_append ignores H_q.
+ */
+typedef struct gdr_kv_dims {
+  int32_t B, T, H_q, H_kv, D, page, n_pages, max_pages;
+} gdr_kv_dims;
+
+/*
+ * gdr_kv_append -- writes the keys and values of up to T new tokens per row
+ * into their pages.  A page's scale is the smallest power of two s >= 2^-100
+ * with max|x| <= 448 s over the finite values written; where the page already
+ * holds tokens of the row (positions before pos) it is at least the scale it
+ * had, and if it grows, their codes are rounded to the new scale (exact but
+ * for values that become subnormal).  Codes round to nearest even; infinities
+ * become +-448, NaN stays NaN.  Slots behind the last new token keep their
+ * codes.
+ *
+ *   k, v         [B,T,H_kv,D] io dtype
+ *   pos          [B] int32
+ *   lens         [B] int32 or NULL
+ *   caches, scales   updated in place; must not overlap an input.  Pages that
+ *                the call writes must belong to one row each (two rows that
+ *                write one page race, and its contents are then undefined)
+ */
+int gdr_kv_append(const gdr_kv_dims* dims, gdr_dtype io, const void* k, const void* v,
+                  const int32_t* block_table, const int32_t* pos, const int32_t* lens,
+                  void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                  hipStream_t stream);
+
+/* gdr_attn_workspace_size -- bytes of device workspace gdr_attn_cached needs
+ * (may be 0); 0 as well for unsupported arguments.  n_pages is not used. */
+size_t gdr_attn_workspace_size(const gdr_kv_dims* dims, gdr_dtype io);
+
+/*
+ * gdr_attn_cached -- softmax attention of T new tokens per row over the cache:
+ * token t of row b, at position pos[b] + t, attends to the cached positions
+ * 0 ... pos[b] + t (append the new tokens first); query head h reads kv head
+ * h / (H_q / H_kv).
+ *
+ *     o = sum_j softmax_j(scale q . k_j) v_j
+ *
+ * A query with nothing to attend to gives zeros.  What lies in the pages
+ * behind a row's last position does not matter, NaN included.
+ *
+ *   q          [B,T,H_q,D] io dtype
+ *   o          [B,T,H_q,D] io dtype; must not overlap any input
+ *   workspace  gdr_attn_workspace_size() bytes (NULL if that is 0), 16-byte
+ *              aligned, uninitialised, overlapping nothing else; one for each
+ *              call that may run at the same time
+ */
+int gdr_attn_cached(const gdr_kv_dims* dims, gdr_dtype io, const void* q, const void* k_cache,
+                    const void* v_cache, const float* k_scale, const float* v_scale,
+                    const int32_t* block_table, const int32_t* pos, const int32_t* lens, void* o,
+                    float scale, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Static, human-readable text for a gdr_status value. */
 const char* gdr_strerror(int status);

@@ -1,0 +1,199 @@
+"""The selective state space scan on the GPU against its 64-bit token recurrence."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_40_amd as gdr
+from tests import layer_ref as ref
+from tests.gpu_util import DEV, announce, io_dtype, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+EPS = 2.0 ** -24
+
+
+def inputs(seed, B, T, G, H, N, P, io, strong=False):
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    dt = io_dtype(io)
+    return dict(x=r(B, T, H, P).to(dt), b=r(B, T, G, N).to(dt), c=r(B, T, G, N).to(dt),
+                dt=r(B, T, H) * (6.0 if strong else 1.0),
+                A_log=torch.log(1 + 15 * torch.rand(H, generator=gen)),
+                dt_bias=torch.full((H,), 0.0 if strong else -3.0) + 0.5 * r(H), D=r(H)), \
+        0.2 * r(B, H, N, P)
+
+
+def up(d):
+    return {k: None if v is None else v.to(DEV) for k, v in d.items()}
+
+
+def prefill(d, s_in, G, lens=None, in_place=False, ws_fill=None):
+    """y and the state of one call, every output filled with 7 before it."""
+    B, T, H, P = d["x"].shape
+    N = d["b"].shape[3]
+    g = up(d)
+    s = None if s_in is None else s_in.to(DEV)
+    s_out = s if in_place else torch.full((B, H, N, P), 7.0, device=DEV)
+    y = torch.full_like(g["x"], 7.0)
+    size = dict(G=G, H=H, N=N, P=P)
+    n = gdr.gdr_ssm_workspace_size(B, T, io_dtype=d["x"].dtype, **size)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV) if n else None   # NaN as floats
+    gl = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=DEV)
+    gdr.gdr_ssm_prefill(g["x"], g["b"], g["c"], g["dt"], g["A_log"], g["dt_bias"], g["D"], s, s_out,
+                        y, ws, lens=gl, **size)
+    torch.cuda.synchronize()
+    return y.cpu(), s_out.cpu()
+
+
+def check(d, s_in, got, lens=None):
+    B, T = d["x"].shape[:2]
+    N, io = d["b"].shape[3], d["x"].dtype
+    want, mag, S, M = ref.ssm(**d, state=s_in, lens=lens)
+    y, s = got
+    # fp32: a term is off by ssm_units at most.  bf16: the output rounds by
+    # half a step of its value, and in the chunk form each weight and each
+    # state element rounds by half a step of its own before its product.
+    bound = ref.ssm_units(T, N) * EPS * mag + 1e-30
+    if io == torch.bfloat16:
+        bound = bound + 2.0 ** -8 * (want.abs() + mag)
+    ns = ref.clip_lens(lens, B, T)
+    for b, n in enumerate(ns):
+        assert ref.worst(y[b, :n], want[b, :n], bound[b, :n]) <= 1
+        assert (y[b, n:] == 7).all()
+    assert ref.worst(s, S, ref.ssm_units(T, N) * EPS * M + 1e-30) <= 1
+    # Over the whole tensor the roundings add up as independent ones: the
+    # output's, the weights' and the state's, each uniform over half a step.
+    keep = torch.tensor([[t < n for t in range(T)] for n in ns])
+    if keep.any():
+        assert ref.rel(y[keep], want[keep]) <= (2.0 ** -8 if io == torch.bfloat16
+                                                 else ref.ssm_norm(T, N))
+    if S.norm() > 0:
+        assert ref.rel(s, S) <= ref.ssm_norm(T, N)
+
+
+# Around the chunk of 64 tokens, one token, one head, shared and own groups.
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,G,H,N,P", [
+    (1, 1, 1, 1, 16, 16), (2, 5, 1, 2, 32, 16), (1, 16, 2, 2, 64, 32), (2, 63, 1, 3, 16, 64),
+    (1, 64, 2, 4, 128, 64), (1, 65, 1, 2, 64, 128), (3, 100, 2, 6, 32, 16), (1, 129, 1, 1, 128, 128),
+    (2, 200, 4, 4, 16, 32), (1, 321, 1, 5, 128, 32), (2, 257, 1, 2, 32, 128), (1, 640, 1, 8, 64, 64)])
+def test_prefill(B, T, G, H, N, P, io):
+    require_gpu()
+    announce(f"ssm prefill B={B} T={T} G={G} H={H} N={N} P={P} io={io}")
+    d, s0 = inputs(T + 7 * N, B, T, G, H, N, P, io)
+    check(d, s0, prefill(d, s0, G))
+    check(d, None, prefill(d, None, G))
+    lens = [T // 2, T + 9, -1][:B]
+    check(d, s0, prefill(d, s0, G, lens, in_place=True), lens)
+    bare = dict(d, dt_bias=None, D=None)
+    check(bare, s0, prefill(bare, s0, G))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("N,P", [(16, 16), (16, 128), (32, 64), (64, 16), (128, 32), (128, 128)])
+def test_every_width(N, P, io):
+    require_gpu()
+    announce(f"ssm widths N={N} P={P} io={io}")
+    d, s0 = inputs(N + P, 2, 150, 2, 4, N, P, io)
+    check(d, s0, prefill(d, s0, 2, [150, 77]), [150, 77])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_strong_and_mixed_decay(io):
+    """Step sizes from about 0 to 20 at rates up to 16: a chunk decays by up to
+    e^-1e4 between tokens that hardly decay at all."""
+    require_gpu()
+    announce(f"ssm strong decay io={io}")
+    d, s0 = inputs(5, 2, 200, 1, 4, 32, 32, io, strong=True)
+    check(d, s0, prefill(d, s0, 1))
+    d["dt"][:, 10:14] = 60.0
+    d["dt"][:, 70:74] = -60.0
+    check(d, s0, prefill(d, s0, 1))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_weak_decay_keeps_the_first_token(io):
+    require_gpu()
+    announce(f"ssm weak decay io={io}")
+    d, s0 = inputs(6, 1, 700, 1, 2, 16, 32, io)
+    d["A_log"] = torch.full((2,), math.log(1e-3))
+    d["dt_bias"] = torch.full((2,), -6.0)
+    check(d, s0, prefill(d, s0, 1))
+
+
+@pytest.mark.parametrize("B,H,T", [(1, 2, 4097), (1, 24, 1500), (40, 8, 130)])
+def test_few_and_many_workgroups(B, H, T):
+    """Long sequences over few heads (cut into parts), and wide batches."""
+    require_gpu()
+    announce(f"ssm B={B} H={H} T={T}")
+    d, s0 = inputs(T, B, T, 1, H, 64, 64, "bf16")
+    lens = None if B == 1 else [(i * 37) % (T + 1) for i in range(B)]
+    check(d, s0, prefill(d, s0, 1, lens), lens)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,G,H,N,P", [
+    (1, 1, 1, 16, 16), (3, 2, 4, 16, 32), (2, 1, 3, 32, 16), (5, 4, 4, 64, 64), (1, 1, 32, 128, 64),
+    (2, 2, 8, 128, 128), (3, 1, 2, 32, 128), (2, 1, 2, 128, 16), (64, 1, 4, 64, 128)])
+def test_steps(B, G, H, N, P, io):
+    require_gpu()
+    announce(f"ssm steps B={B} G={G} H={H} N={N} P={P} io={io}")
+    T = 4
+    d, s0 = inputs(B + N, B, T, G, H, N, P, io)
+    for bare in (False, True):
+        d = dict(d, dt_bias=None, D=None) if bare else d
+        g, S = up(d), s0.to(DEV)
+        y = torch.empty((B, H, P), dtype=g["x"].dtype, device=DEV)
+        ys = []
+        for t in range(T):
+            xbc = torch.cat([g[k][:, t].flatten(1) for k in ("x", "b", "c")], 1).contiguous()
+            gdr.gdr_ssm_step(xbc, g["dt"][:, t].contiguous(), g["A_log"], g["dt_bias"], g["D"], S,
+                             y, G=G, H=H, N=N, P=P)
+            ys.append(y.cpu())
+        check(d, s0, (torch.stack(ys, 1), S.cpu()))
+
+
+def test_no_tokens_copies_the_state():
+    require_gpu()
+    announce("ssm T=0 and B=0")
+    d, s0 = inputs(2, 2, 0, 1, 2, 32, 32, "bf16")
+    _, s = prefill(d, s0, 1)
+    assert torch.equal(s, s0)
+    _, s = prefill(d, None, 1)
+    assert (s == 0).all()
+    d, s0 = inputs(2, 0, 5, 1, 2, 32, 32, "bf16")
+    prefill(d, s0, 1)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_nan_behind_a_rows_end_does_not_matter(io):
+    require_gpu()
+    announce(f"ssm NaN padding io={io}")
+    d, s0 = inputs(9, 2, 150, 1, 2, 32, 32, io)
+    lens = [70, 129]
+    clean = prefill(d, s0, 1, lens)
+    for k in ("x", "b", "c", "dt"):
+        for i, n in enumerate(lens):
+            d[k][i, n:] = float("nan")
+    got = prefill(d, s0, 1, lens)
+    assert all(torch.equal(a, b) for a, b in zip(got, clean))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [40, 200])
+def test_nan_token_does_not_reach_earlier_ones(T, io):
+    require_gpu()
+    announce(f"ssm NaN token T={T} io={io}")
+    d, s0 = inputs(10, 1, T, 2, 4, 32, 64, io)
+    clean, _ = prefill(d, s0, 2)
+    at = T // 2 + 3
+    d["x"][0, at, 1, 5] = float("nan")       # head 1, column 5
+    y, s = prefill(d, s0, 2)
+    assert torch.equal(y[:, :at], clean[:, :at])
+    assert torch.equal(y[:, :, [0, 2, 3]], clean[:, :, [0, 2, 3]])
+    assert torch.isnan(y[0, at:, 1, 5]).all() and torch.isnan(s[0, 1, :, 5]).all()
+    cols = [p for p in range(64) if p != 5]
+    assert torch.equal(y[..., cols], clean[..., cols])
