@@ -117,8 +117,8 @@ int check_kv_sizes(const gdr_kv_dims* d, gdr_dtype io, bool attn) {
   if (attn ? !within(gdr::kMaxGrid, {d->B, d->T, d->H_q})
            : !within(gdr::kMaxGrid, {2, d->B, gdr::kv_touched_pages(d->T, d->page), d->H_kv}))
     return GDR_E_SHAPE;
-  // Positions are 32-bit.
-  if (!within(INT32_MAX, {d->max_pages, d->page})) return GDR_E_SHAPE;
+  // Positions, and the end of the step they fall into, are 32-bit.
+  if (!within(INT32_MAX - 128, {d->max_pages, d->page})) return GDR_E_SHAPE;
   if (!within(INT64_MAX / 16, {d->n_pages, d->H_kv, d->page, d->D})) return GDR_E_SHAPE;
   return GDR_OK;
 }

@@ -268,3 +268,27 @@ def test_pages_shared_by_rows():
     q = torch.randn(3, 4, 4, 128).to(torch.bfloat16)
     pos = [50, 44, 59]
     check(c, q, attend(c, q, pos, 0.1), pos, 0.1)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,T", [(4, 6), (2, 100)])
+def test_nan_token_does_not_reach_earlier_queries(Hq, T, io):
+    """A new token whose key or value holds NaN: queries before it do not see it."""
+    require_gpu()
+    announce(f"attention with a NaN token Hq={Hq} T={T} io={io}")
+    c = Cache(13, 2, 12, 2, 64, 16)
+    q = torch.randn(2, T, Hq, 64).to(io_dtype(io))
+    pos = [37, 64]
+    clean = attend(c, q, pos, 0.125)
+    at = T // 2
+    for b in range(2):
+        p = pos[b] + at
+        pg, sl = int(c.table[b, p // 16]), p % 16
+        c.vc[pg, 0, 7, sl] = math.nan                    # head 0: one column of the value
+        c.kc[pg, 1, sl, 3] = math.nan                    # head 1: the key
+    o = attend(c, q, pos, 0.125)
+    half = Hq // 2
+    assert torch.equal(o[:, :at], clean[:, :at])
+    cols = [d for d in range(64) if d != 7]
+    assert torch.equal(o[:, :, :half][..., cols], clean[:, :, :half][..., cols])
+    assert torch.isnan(o[:, at:, :half, 7]).all() and torch.isnan(o[:, at:, half:]).all()
