@@ -111,6 +111,9 @@ struct SsmArgs {
 };
 hipError_t launch_ssm_step(const SsmArgs& a, int io_bf16, hipStream_t stream);
 size_t ssm_workspace_bytes(int B, int T, int G, int H, int N, int P, int io_bf16);
+// Longest prompt that is walked token by token; longer ones go in chunks.
+int ssm_walk_max_t();
+hipError_t launch_ssm_chunked(const SsmArgs& a, int io_bf16, hipStream_t stream);
 hipError_t launch_ssm_prefill(const SsmArgs& a, int io_bf16, hipStream_t stream);
 
 // Argument blocks of the 8-bit cache.

@@ -155,6 +155,8 @@ __global__ __launch_bounds__(64) void ssm_walk_kernel(SsmArgs a) {
   for (int m = 0; m < RPT; ++m) *reinterpret_cast<float4*>(a.state_out + at + m * a.P) = s[m];
 }
 
+constexpr int kWalkMaxT = 16;
+
 template <typename T, int N>
 hipError_t step_n(const SsmArgs& a, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.B) * a.H);
@@ -209,9 +211,10 @@ hipError_t launch_ssm_step(const SsmArgs& a, int io_bf16, hipStream_t stream) {
   return io_bf16 ? step_t<bf16>(a, stream) : step_t<float>(a, stream);
 }
 
-size_t ssm_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
+int ssm_walk_max_t() { return kWalkMaxT; }
 
 hipError_t launch_ssm_prefill(const SsmArgs& a, int io_bf16, hipStream_t stream) {
+  if (a.T > kWalkMaxT) return launch_ssm_chunked(a, io_bf16, stream);
   return io_bf16 ? walk_t<bf16>(a, stream) : walk_t<float>(a, stream);
 }
 
