@@ -88,6 +88,9 @@ int check_ssm_sizes(const gdr_ssm_dims* d, gdr_dtype io, int T) {
   if (d->B < 0 || T < 0 || d->G <= 0 || d->H <= 0 || d->N <= 0 || d->P <= 0) return GDR_E_SHAPE;
   if (d->H % d->G != 0) return GDR_E_SHAPE;
   if (!supported_width(d->N) || !supported_width(d->P)) return GDR_E_UNSUPPORTED;
+  // The rows of a chunk of 64 tokens are reached through 32-bit byte offsets.
+  if (!within(UINT32_MAX, {64, 4, d->H, d->P}) || !within(UINT32_MAX, {64, 4, d->G, d->N}))
+    return GDR_E_SHAPE;
   // Workgroups: one per (row, head, 16 columns, chunk of 64 tokens) at most.
   const long long chunks = (static_cast<long long>(T) + 63) / 64;
   if (!within(gdr::kMaxGrid, {d->B, d->H, d->P / 16, chunks > 0 ? chunks : 1}))

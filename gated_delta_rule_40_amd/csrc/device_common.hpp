@@ -150,4 +150,21 @@ __device__ __forceinline__ float silu_hw(float x) {
   return x * __builtin_amdgcn_rcpf(1.0f + exp_hw(-x));
 }
 
+// softplus(z) = max(z, 0) + log1p(u) with u = e^-|z| in (0, 1], to a few units
+// in the last place: log1p(u) = 2 atanh(s), s = u / (2 + u) <= 1/3, by the odd
+// series of atanh (its first term left out, s^17 / 17, is below 2^-30 of s).
+__device__ __forceinline__ float softplus_hw(float z) {
+  const float u = exp_hw(-__builtin_fabsf(z));
+  const float s = u * __builtin_amdgcn_rcpf(2.0f + u), q = s * s;
+  float p = 1.0f / 15.0f;
+  p = __builtin_fmaf(p, q, 1.0f / 13.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 11.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 9.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 7.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 5.0f);
+  p = __builtin_fmaf(p, q, 1.0f / 3.0f);
+  p = __builtin_fmaf(p * q, s, s);
+  return (z > 0.0f ? z : 0.0f * z) + 2.0f * p;  // NaN stays
+}
+
 }  // namespace gdr

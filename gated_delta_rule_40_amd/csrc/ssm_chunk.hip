@@ -9,7 +9,7 @@
 // and kept as two floats, so that differences late in a strongly decaying
 // chunk stay exact.
 //
-// A workgroup owns 16 columns per wave of the state of a group's heads (the
+// A workgroup owns 16 CT columns per wave of the state of a group's heads (the
 // r P columns of the r = H / G heads that share B and C lie side by side in x
 // and y) and walks the chunks in order with the state in matrix accumulators.
 // Per chunk:
@@ -48,7 +48,16 @@ typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int L = 64;  // tokens per chunk
+
+// 16 bytes, or zeros.
+__device__ __forceinline__ u32x4 load16_if(bool in, const void* p) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (in) v = *static_cast<const u32x4*>(p);
+  return v;
+}
 
 // Matrix operands of one io type, KS the width of a contraction step.  Lane l supplies row l % 16 with g = l / 16.
 template <typename T>
@@ -84,7 +93,7 @@ struct Op<bf16> {
     return *reinterpret_cast<const F*>(row + 32 * s + 8 * g);
   }
   // Eight values from column c (a multiple of 8) of a row, to their places.
-  __device__ static __forceinline__ void store_ordered(bf16* row, int c, uint4 v) {
+  __device__ static __forceinline__ void store_ordered(bf16* row, int c, u32x4 v) {
     bf16* p = row + (c & ~31) + 4 * ((c & 31) / 16) + 2 * (c & 15);
     *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
     *reinterpret_cast<uint2*>(p + 8) = make_uint2(v.z, v.w);
@@ -96,10 +105,12 @@ struct Op<bf16> {
   // Columns col0 + r of tokens 32 s + 8 g ... + 7: a transposing load takes 4
   // tokens x 16 columns for each lane group, its lane r addressing token r / 4
   // and columns 4 (r % 4), and hands lane r column r.
+  // SHIFT: what every other eight rows lie further by.
+  template <int SHIFT>
   __device__ static __forceinline__ F columns(const bf16* buf, int ld, int s, int g, int r,
                                               int col0) {
     typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-    const bf16* p = buf + (32 * s + 8 * g + r / 4) * ld + col0 + 4 * (r & 3);
+    const bf16* p = buf + (32 * s + 8 * g + r / 4) * ld + (g & 1) * SHIFT + col0 + 4 * (r & 3);
     const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
     const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ld));
     return join(__builtin_bit_cast(bf16x4_t, a), __builtin_bit_cast(bf16x4_t, b));
@@ -111,12 +122,18 @@ struct Op<bf16> {
     const float4 w1 = *reinterpret_cast<const float4*>(w + 32 * s + 8 * g + 4);
     const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v = static_cast<float>(x[i]) * ww[i];
+    for (int i = 0; i < 8; i += 2) {
+      float v0 = static_cast<float>(x[i]) * ww[i], v1 = static_cast<float>(x[i + 1]) * ww[i + 1];
 #pragma unroll
       for (int q = 0; q < PIECES; ++q) {
-        out[q][i] = static_cast<bf16>(v);
-        v -= static_cast<float>(out[q][i]);
+        typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        const bf16x2_t h = __builtin_convertvector((f32x2{v0, v1}), bf16x2_t);
+        out[q][i] = h[0];
+        out[q][i + 1] = h[1];
+        const unsigned u = __builtin_bit_cast(unsigned, h);
+        v0 -= __builtin_bit_cast(float, u << 16);
+        v1 -= __builtin_bit_cast(float, u & 0xffff0000u);
       }
     }
   }
@@ -143,15 +160,16 @@ struct Op<float> {
   __device__ static __forceinline__ F rows_ordered(const float* row, int s, int g) {
     return rows(row, s, g);
   }
-  __device__ static __forceinline__ void store_ordered(float* row, int c, uint4 v) {
-    *reinterpret_cast<uint4*>(row + c) = v;
+  __device__ static __forceinline__ void store_ordered(float* row, int c, u32x4 v) {
+    *reinterpret_cast<u32x4*>(row + c) = v;
   }
   __device__ static __forceinline__ F tokens(const float* row, int s, int g) {
     return row[4 * s + g];
   }
+  template <int SHIFT>
   __device__ static __forceinline__ F columns(const float* buf, int ld, int s, int g, int r,
                                               int col0) {
-    return buf[(4 * s + g) * ld + col0 + r];
+    return buf[(4 * s + g) * ld + ((s >> 1) & 1) * SHIFT + col0 + r];
   }
   __device__ static __forceinline__ void weigh(F x, const float* w, int s, int g,
                                                F (&out)[PIECES]) {
@@ -162,25 +180,41 @@ struct Op<float> {
   }
 };
 
-// HB heads of the workgroup's 16 NW columns.
-template <typename T, int N, int HB, int NW>
+// What a token of a head contributes by, Gamma in units of log2.
+struct Rows {
+  float gh[L], gl[L];  // Gamma as two floats
+  float d[L];          // step size
+  float eg[L];         // e^Gamma
+  float w[L];          // e^(Gamma_L - Gamma) d
+  float rf[L];         // e^(Gamma - Gamma_m), m the last token before its 16
+  float cf[96];        // e^(Gamma_m - Gamma) d of the tokens up to m, for m = 15, 31, 47
+  // Where the m of tile row ti (1, 2, 3) begin.
+  __device__ static __forceinline__ int at(int ti) { return 8 * ti * (ti - 1); }
+};
+
+// A workgroup's LDS: NW waves of CT 16-column tiles, over HB heads.  The row
+// pitches keep the 16-byte reads of 16 rows (C, P) and the transposing reads
+// of 4 rows (B, x: 32 bytes a row, a pitch of 32 bytes more than a multiple of
+// 256) on distinct banks; B is also read 8 bytes from each of 16 rows, for
+// which every other eight rows lie 16 bytes further.
+template <typename T, int N, int HB, int NW, int CT, bool kStates>
 struct Shape {
   static constexpr int EV = 16 / static_cast<int>(sizeof(T));  // values per 16 bytes
   static constexpr int NP = N < Op<T>::KS ? Op<T>::KS : N;     // rows of the state, padded
-  static constexpr int COLS = 16 * NW;
+  static constexpr int COLS = 16 * NW * CT;
   static constexpr int NT = 64 * NW;
-  static constexpr int LB = NP + EV;    // row pitches in LDS, 16-byte multiples
-  static constexpr int LX = COLS + EV;
-  static constexpr int LP = L + EV;
-  static constexpr int BV = (L * (N / EV) + NT - 1) / NT;      // 16-byte loads per thread
+  static constexpr int LB = NP + 2 * EV, LC = NP + EV, LX = COLS + (COLS % 128 ? 1 : 2) * EV,
+                       LP = L + EV;
+  static constexpr int BV = (L * (N / EV) + NT - 1) / NT;  // 16-byte loads per thread
   static constexpr int XV = (L * (COLS / EV) + NT - 1) / NT;
+  static_assert(HB <= NW, "a wave forms the rows of one head at a time");
+  Rows rows[2][HB];
   T b[L][LB];
-  T c[L][LB];
   T x[L][LX];
-  T p[HB][L][LP];
-  // Per head and token: Gamma log2(e) in two floats, d, e^Gamma, and
-  // e^(Gamma_L - Gamma) d.
-  float gh[HB][L], gl[HB][L], d[HB][L], eg[HB][L], w[HB][L];
+  T c[kStates ? 1 : L][LC];
+  T p[kStates ? 1 : HB][L][LP];
+  float rate[HB], db[HB];  // -exp(A_log), dt_bias
+  __device__ __forceinline__ T* brow(int row) { return b[row] + ((row >> 3) & 1) * EV; }
 };
 
 // Workgroups that share B and C (neighbouring numbers) go to one XCD: hardware
@@ -190,18 +224,64 @@ __device__ __forceinline__ unsigned xcd_order(unsigned id, unsigned total) {
   return xcd * per + min(xcd, rem) + k;
 }
 
+// The lane's 64-bit value from another lane of the wave by a DPP move (0 where
+// there is none).
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double dpp_from(double x) {
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+  const unsigned lo = __builtin_amdgcn_update_dpp(0u, static_cast<unsigned>(u), kCtrl, kRows, 0xf, false);
+  const unsigned hi =
+      __builtin_amdgcn_update_dpp(0u, static_cast<unsigned>(u >> 32), kCtrl, kRows, 0xf, false);
+  return __builtin_bit_cast(double, static_cast<unsigned long long>(hi) << 32 | lo);
+}
+
+// Inclusive prefix sum over the wave: row shifts inside each 16 lanes, then
+// the last lanes of rows 0 and 2 to rows 1 and 3, then lane 31 to the upper half.
+__device__ __forceinline__ double wave_prefix_sum(double x) {
+  x += dpp_from<0x111, 0xf>(x);  // row_shr:1
+  x += dpp_from<0x112, 0xf>(x);
+  x += dpp_from<0x114, 0xf>(x);
+  x += dpp_from<0x118, 0xf>(x);
+  x += dpp_from<0x142, 0xa>(x);  // row_bcast:15
+  x += dpp_from<0x143, 0xc>(x);  // row_bcast:31
+  return x;
+}
+
+// The rows of one head's chunk: lane = token, z = dt + dt_bias (d = 0 where the
+// token is not there).
+__device__ __forceinline__ void form_rows(Rows& o, int lane, bool there, float z, float rate) {
+  const float d = there ? softplus_hw(z) : 0.0f;
+  const double gam = wave_prefix_sum(static_cast<double>(rate) * d * 1.4426950408889634);
+  const float hi = static_cast<float>(gam);
+  o.gh[lane] = hi;
+  o.gl[lane] = static_cast<float>(gam - static_cast<double>(hi));
+  o.d[lane] = d;
+  o.eg[lane] = __builtin_amdgcn_exp2f(hi);
+  o.w[lane] = __builtin_amdgcn_exp2f(static_cast<float>(__shfl(gam, 63, 64) - gam)) * d;
+  double before = 0.0;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const double m = __shfl(gam, 16 * k + 15, 64);
+    if (lane / 16 == k + 1) before = m;
+    if (lane < 16 * k + 16)
+      o.cf[Rows::at(k + 1) + lane] = __builtin_amdgcn_exp2f(static_cast<float>(m - gam)) * d;
+  }
+  o.rf[lane] = __builtin_amdgcn_exp2f(static_cast<float>(gam - before));
+}
+
 // kStates: the first pass (segment states from zero).  ws: segment starts
 // [B,H,segs,N,P], then segment log2 decays [B,H,segs].
-template <typename T, int N, int HB, int NW, bool kStates>
-__global__ __launch_bounds__(64 * NW) void ssm_chunk_kernel(SsmArgs a, int blocks, int segs,
-                                                            int seg_chunks) {
-  using Sh = Shape<T, N, HB, NW>;
+template <typename T, int N, int HB, int NW, int CT, bool kStates>
+__global__ __launch_bounds__(64 * NW, 2) void ssm_chunk_kernel(SsmArgs a, int blocks, int segs,
+                                                               int seg_chunks) {
+  using Sh = Shape<T, N, HB, NW, CT, kStates>;
   using O = Op<T>;
   using F = typename O::F;
   constexpr int KN = Sh::NP / O::KS, KL = L / O::KS, NTL = Sh::NP / 16, EV = Sh::EV;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   Sh& sm = *reinterpret_cast<Sh*>(smem);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // scalar: so is what follows from it
   const int r = lane & 15, g = lane >> 4;
 
   const int pass_segs = kStates ? segs - 1 : segs;
@@ -220,46 +300,65 @@ __global__ __launch_bounds__(64 * NW) void ssm_chunk_kernel(SsmArgs a, int block
   const int width = rh * a.P;              // its columns
   const int col0 = block * Sh::COLS;       // of the workgroup, in the group
   const int hb0 = col0 / a.P;              // its first head, in the group
-  const int wcol = col0 + 16 * wave;       // of the wave
-  const bool on = wcol < width;
-  const int hw = on ? wcol / a.P - hb0 : 0;  // the wave's head in the workgroup
-  const int head = grp * rh + min(wcol / a.P, rh - 1);
-  const int pcol = wcol % a.P;
+  // The wave's columns: all of one head (P is a multiple of 16 CT).
+  const int lcol = 16 * CT * wave;         // in the workgroup
+  const bool on = col0 + lcol < width;
+  const int hw = on ? (col0 + lcol) / a.P - hb0 : 0;
+  const int head = grp * rh + min((col0 + lcol) / a.P, rh - 1);
+  const int pcol = (col0 + lcol) % a.P;
 
-  // Loads of one chunk, a chunk ahead.
-  uint4 pb[Sh::BV], pc[kStates ? 1 : Sh::BV], px[Sh::XV];
-  float pdt[(HB + NW - 1) / NW];
+  // Loads of one chunk, a chunk ahead: thread tid takes 16 bytes of row row_b +
+  // i * kStepB of B and C (and likewise x), through one 32-bit lane offset each
+  // from bases that are the same for all lanes.
+  constexpr int kRowB = N / EV, kRowX = Sh::COLS / EV;  // 16-byte pieces of a row
+  constexpr int kStepB = Sh::NT / kRowB, kStepX = Sh::NT / kRowX;
+  static_assert(Sh::NT % kRowB == 0 && Sh::NT % kRowX == 0, "whole rows per pass");
+  u32x4 pb[Sh::BV], pc[kStates ? 1 : Sh::BV], px[Sh::XV];
   const size_t brow = static_cast<size_t>(a.G) * N, xrow = static_cast<size_t>(a.H) * a.P;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const int row_b = tid / kRowB, cc_b = tid % kRowB * EV;
+  const int row_x = tid / kRowX, cc_x = tid % kRowX * EV;
+  const unsigned off_b = (row_b * static_cast<unsigned>(brow) + cc_b) * sizeof(T);
+  const unsigned off_x = (row_x * static_cast<unsigned>(xrow) + cc_x) * sizeof(T);
+  const bool in_x = col0 + cc_x < width;
+  // Every thread has something to load from every whole chunk.
+  const bool in_all = col0 + Sh::COLS <= width && L % kStepB == 0 && L % kStepX == 0;
   auto request = [&](int chunk) {
-    const int t0 = chunk * L;
-    const size_t base = static_cast<size_t>(b) * a.T + t0;
-    const T* bp = static_cast<const T*>(a.b) + base * brow + grp * N;
-    const T* cp = static_cast<const T*>(a.c) + base * brow + grp * N;
-    const T* xp = static_cast<const T*>(a.x) + base * xrow + static_cast<size_t>(grp) * width + col0;
+    const int left = n - chunk * L;  // tokens from here on
+    const size_t base = static_cast<size_t>(b) * a.T + static_cast<size_t>(chunk) * L;
+    const char* bp = reinterpret_cast<const char*>(static_cast<const T*>(a.b) + base * brow + grp * N);
+    const char* cp = reinterpret_cast<const char*>(static_cast<const T*>(a.c) + base * brow + grp * N);
+    const char* xp = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + base * xrow +
+                                                   static_cast<size_t>(grp) * width + col0);
+    if (left >= L && in_all) {
+#pragma unroll
+      for (int i = 0; i < Sh::BV; ++i) {
+        const size_t step = i * kStepB * brow * sizeof(T);
+        pb[i] = *reinterpret_cast<const u32x4*>(bp + step + off_b);
+        if constexpr (!kStates) pc[i] = *reinterpret_cast<const u32x4*>(cp + step + off_b);
+      }
+#pragma unroll
+      for (int i = 0; i < Sh::XV; ++i)
+        px[i] = *reinterpret_cast<const u32x4*>(xp + i * kStepX * xrow * sizeof(T) + off_x);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < Sh::BV; ++i) {
-      const int u = tid + i * Sh::NT, row = u / (N / EV), cc = u % (N / EV) * EV;
-      const bool in = row < L && t0 + row < n;
-      pb[i] = in ? *reinterpret_cast<const uint4*>(bp + row * brow + cc) : zero;
-      if constexpr (!kStates) pc[i] = in ? *reinterpret_cast<const uint4*>(cp + row * brow + cc) : zero;
+      const int row = row_b + i * kStepB;
+      const bool in = row < L && row < left;
+      const size_t step = i * kStepB * brow * sizeof(T);
+      pb[i] = load16_if(in, bp + step + off_b);
+      if constexpr (!kStates) pc[i] = load16_if(in, cp + step + off_b);
     }
 #pragma unroll
     for (int i = 0; i < Sh::XV; ++i) {
-      const int u = tid + i * Sh::NT, row = u / (Sh::COLS / EV), cc = u % (Sh::COLS / EV) * EV;
-      const bool in = row < L && t0 + row < n && col0 + cc < width;
-      px[i] = in ? *reinterpret_cast<const uint4*>(xp + row * xrow + cc) : zero;
-    }
-#pragma unroll
-    for (int i = 0; i < (HB + NW - 1) / NW; ++i) {
-      const int h = hb0 + wave + i * NW;
-      const bool in = wave + i * NW < HB && h < rh && t0 + lane < n;
-      pdt[i] = in ? a.dt[(base + lane) * a.H + grp * rh + h] : 0.0f;
+      const int row = row_x + i * kStepX;
+      px[i] = load16_if(in_x && row < L && row < left,
+                        xp + i * kStepX * xrow * sizeof(T) + off_x);
     }
   };
 
-  // The state: rows 16 k + 4 g + e, column pcol + r.
-  f32x4 S[NTL];
+  // The state: rows 16 k + 4 g + e, column pcol + 16 ct + r.
+  f32x4 S[CT][NTL];
   const size_t unit = static_cast<size_t>(b) * a.H + head;
   float* starts = static_cast<float*>(a.ws);
   float* decays = starts + static_cast<size_t>(a.B) * a.H * segs * N * a.P;
@@ -269,70 +368,77 @@ __global__ __launch_bounds__(64 * NW) void ssm_chunk_kernel(SsmArgs a, int block
     else if (a.state_in) from = a.state_in + unit * N * a.P;
   }
 #pragma unroll
-  for (int k = 0; k < NTL; ++k)
+  for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = 16 * k + 4 * g + e;
-      S[k][e] = from && on && row < N ? from[static_cast<size_t>(row) * a.P + pcol + r] : 0.0f;
-    }
+    for (int k = 0; k < NTL; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = 16 * k + 4 * g + e;
+        S[ct][k][e] = from && on && row < N
+                          ? from[static_cast<size_t>(row) * a.P + pcol + 16 * ct + r]
+                          : 0.0f;
+      }
 
   if constexpr (Sh::NP > N) {  // the columns that the loads never write stay zeros
     for (int i = tid; i < L * Sh::NP; i += Sh::NT) {
-      sm.b[i / Sh::NP][i % Sh::NP] = from_f32<T>(0.0f);
-      sm.c[i / Sh::NP][i % Sh::NP] = from_f32<T>(0.0f);
+      sm.brow(i / Sh::NP)[i % Sh::NP] = from_f32<T>(0.0f);
+      if constexpr (!kStates) sm.c[i / Sh::NP][i % Sh::NP] = from_f32<T>(0.0f);
     }
     __syncthreads();
   }
 
-  float rate[(HB + NW - 1) / NW], db[(HB + NW - 1) / NW];
-  const float dskip = !kStates && a.D && on ? a.D[head] : 0.0f;
-#pragma unroll
-  for (int i = 0; i < (HB + NW - 1) / NW; ++i) {
-    const int h = min(hb0 + wave + i * NW, rh - 1);
-    rate[i] = -expf(a.A_log[grp * rh + h]);
-    db[i] = a.dt_bias ? a.dt_bias[grp * rh + h] : 0.0f;
+  for (int hb = tid; hb < HB; hb += Sh::NT) {
+    const int h = grp * rh + min(hb0 + hb, rh - 1);
+    sm.rate[hb] = -expf(a.A_log[h]);
+    sm.db[hb] = a.dt_bias ? a.dt_bias[h] : 0.0f;
   }
+  __syncthreads();
+  // The waves take turns at forming the rows of the next chunk's heads: wave
+  // (hb + HB chunk) mod NW forms head hb's.
+  auto turn = [&](int chunk) { return (wave + NW - (HB * chunk) % NW) % NW; };
+  float pdt = 0.0f;
+  auto request_dt = [&](int chunk) {
+    const int hb = turn(chunk), t = chunk * L + lane;
+    pdt = hb < HB && hb0 + hb < rh && t < n
+              ? a.dt[(static_cast<size_t>(b) * a.T + t) * a.H + grp * rh + hb0 + hb]
+              : 0.0f;
+  };
+  auto rows_of = [&](int chunk) {
+    const int hb = turn(chunk);
+    if (hb < HB)
+      form_rows(sm.rows[chunk & 1][hb], lane, chunk * L + lane < n, pdt + sm.db[hb], sm.rate[hb]);
+  };
+  const unsigned off_y =
+      (r * static_cast<unsigned>(xrow) + head * a.P + pcol + 4 * g) * sizeof(T);
+  const float dskip = !kStates && a.D && on ? a.D[head] : 0.0f;
   double total = 0.0;  // log2 decay of the segment so far (first pass)
 
-  if (first < end) request(first);
+  if (first < end) {
+    request_dt(first);
+    request(first);
+    rows_of(first);
+    if (first + 1 < end) request_dt(first + 1);
+  }
+#pragma unroll 1
   for (int chunk = first; chunk < end; ++chunk) {
     const int t0 = chunk * L;
     // ---- 1. to LDS ----
 #pragma unroll
     for (int i = 0; i < Sh::BV; ++i) {
-      const int u = tid + i * Sh::NT, row = u / (N / EV), cc = u % (N / EV) * EV;
+      const int row = row_b + i * kStepB;
       if (row < L) {
-        *reinterpret_cast<uint4*>(&sm.b[row][cc]) = pb[i];
-        if constexpr (!kStates) O::store_ordered(sm.c[row], cc, pc[i]);
+        *reinterpret_cast<u32x4*>(sm.brow(row) + cc_b) = pb[i];
+        if constexpr (!kStates) O::store_ordered(sm.c[row], cc_b, pc[i]);
       }
     }
 #pragma unroll
     for (int i = 0; i < Sh::XV; ++i) {
-      const int u = tid + i * Sh::NT, row = u / (Sh::COLS / EV), cc = u % (Sh::COLS / EV) * EV;
-      if (row < L) *reinterpret_cast<uint4*>(&sm.x[row][cc]) = px[i];
-    }
-#pragma unroll
-    for (int i = 0; i < (HB + NW - 1) / NW; ++i) {
-      const int hb = wave + i * NW;
-      if (hb < HB) {
-        const float d = t0 + lane < n ? softplusf(pdt[i] + db[i]) : 0.0f;
-        double gam = static_cast<double>(rate[i]) * d * 1.4426950408889634;
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-          const double up = __shfl_up(gam, o, 64);
-          gam += lane >= o ? up : 0.0;
-        }
-        const double last = __shfl(gam, 63, 64);
-        const float hi = static_cast<float>(gam);
-        sm.gh[hb][lane] = hi;
-        sm.gl[hb][lane] = static_cast<float>(gam - static_cast<double>(hi));
-        sm.d[hb][lane] = d;
-        sm.eg[hb][lane] = __builtin_amdgcn_exp2f(hi);
-        sm.w[hb][lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - gam)) * d;
-      }
+      const int row = row_x + i * kStepX;
+      if (row < L) *reinterpret_cast<u32x4*>(&sm.x[row][cc_x]) = px[i];
     }
     __syncthreads();
     if (chunk + 1 < end) request(chunk + 1);
+    const Rows* rows = sm.rows[chunk & 1];
 
     // ---- 2. P ----
     if constexpr (!kStates) {
@@ -344,27 +450,38 @@ __global__ __launch_bounds__(64 * NW) void ssm_chunk_kernel(SsmArgs a, int block
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < KN; ++s)
-          acc = O::mma(O::rows(sm.b[16 * tj + r], s, g), O::rows_ordered(sm.c[16 * ti + r], s, g),
+          acc = O::mma(O::rows(sm.brow(16 * tj + r), s, g), O::rows_ordered(sm.c[16 * ti + r], s, g),
                        acc);
         const int i = 16 * ti + r, j = 16 * tj + 4 * g;
 #pragma unroll
         for (int hb = 0; hb < HB; ++hb) {
-          const float4 h4 = *reinterpret_cast<const float4*>(&sm.gh[hb][j]);
-          const float4 l4 = *reinterpret_cast<const float4*>(&sm.gl[hb][j]);
-          const float4 d4 = *reinterpret_cast<const float4*>(&sm.d[hb][j]);
-          const float hi = sm.gh[hb][i], lo = sm.gl[hb][i];
-          const float jh[4] = {h4.x, h4.y, h4.z, h4.w}, jl[4] = {l4.x, l4.y, l4.z, l4.w};
-          const float jd[4] = {d4.x, d4.y, d4.z, d4.w};
+          const Rows& w = rows[hb];
           float v[4];
+          if (ti > tj) {
+            // e^(Gamma_i - Gamma_j) through the last token before tile row ti.
+            const float4 f4 = *reinterpret_cast<const float4*>(&w.cf[Rows::at(ti) + j]);
+            const float f = w.rf[i];
+            v[0] = acc[0] * f * f4.x;
+            v[1] = acc[1] * f * f4.y;
+            v[2] = acc[2] * f * f4.z;
+            v[3] = acc[3] * f * f4.w;
+          } else {
+            const float4 h4 = *reinterpret_cast<const float4*>(&w.gh[j]);
+            const float4 l4 = *reinterpret_cast<const float4*>(&w.gl[j]);
+            const float4 d4 = *reinterpret_cast<const float4*>(&w.d[j]);
+            const float hi = w.gh[i], lo = w.gl[i];
+            const float jh[4] = {h4.x, h4.y, h4.z, h4.w}, jl[4] = {l4.x, l4.y, l4.z, l4.w};
+            const float jd[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f = __builtin_amdgcn_exp2f((hi - jh[e]) + (lo - jl[e])) * jd[e];
-            v[e] = j + e <= i ? acc[e] * f : 0.0f;
+            for (int e = 0; e < 4; ++e) {
+              const float f = __builtin_amdgcn_exp2f((hi - jh[e]) + (lo - jl[e])) * jd[e];
+              v[e] = j + e <= i ? acc[e] * f : 0.0f;
+            }
+            // The tile right of the diagonal that a step of 32 tokens also takes.
+            if (O::KS > 16 && (ti & 1) == 0)
+              store4<T>(&sm.p[hb][i][j + 16], 0.f, 0.f, 0.f, 0.f);
           }
           store4<T>(&sm.p[hb][i][j], v[0], v[1], v[2], v[3]);
-          // The tile right of the diagonal that a step of 32 tokens also takes.
-          if (O::KS > 16 && ti == tj && (ti & 1) == 0)
-            store4<T>(&sm.p[hb][i][j + 16], 0.f, 0.f, 0.f, 0.f);
         }
       }
       __syncthreads();
@@ -372,63 +489,98 @@ __global__ __launch_bounds__(64 * NW) void ssm_chunk_kernel(SsmArgs a, int block
 
     // ---- 3. this wave's columns ----
     if (on) {
-      F xf[KL];
+      const Rows& w = rows[hw];
+      F xf[CT][KL];
       float sum = 0.0f;
 #pragma unroll
-      for (int s = 0; s < KL; ++s) {
-        xf[s] = O::columns(&sm.x[0][0], Sh::LX, s, g, r, 16 * wave);
-        if constexpr (!kStates) sum = O::probe(xf[s], sum);
-      }
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int s = 0; s < KL; ++s) {
+          xf[ct][s] = O::template columns<0>(&sm.x[0][0], Sh::LX, s, g, r, lcol + 16 * ct);
+          if constexpr (!kStates) sum = O::probe(xf[ct][s], sum);
+        }
       if constexpr (!kStates) {
         // x that is not finite must not reach earlier tokens through the zeros
         // above the diagonal of P: such columns are summed one by one.
         const bool plain = !__any(sum != 0.0f);
-        F sf[KN];
+        char* yp = reinterpret_cast<char*>(static_cast<T*>(a.y) +
+                                           (static_cast<size_t>(b) * a.T + t0) * xrow);
+        F sf[CT][KN];
 #pragma unroll
-        for (int s = 0; s < KN; ++s) sf[s] = O::state(S, s);
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int s = 0; s < KN; ++s) sf[ct][s] = O::state(S[ct], s);
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) {
           const int i = 16 * ti + r;
-          f32x4 y = {0.f, 0.f, 0.f, 0.f};
+          f32x4 y[CT];
 #pragma unroll
-          for (int s = 0; s < KN; ++s) y = O::mma(sf[s], O::rows_ordered(sm.c[i], s, g), y);
-          y *= sm.eg[hw][i];
+          for (int ct = 0; ct < CT; ++ct) y[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < KN; ++s) {
+            const F c = O::rows_ordered(sm.c[i], s, g);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) y[ct] = O::mma(sf[ct][s], c, y[ct]);
+          }
+          const float eg = w.eg[i];
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) y[ct] *= eg;
           if (plain) {
 #pragma unroll
-            for (int s = 0; s * O::KS < 16 * (ti + 1); ++s)
-              y = O::mma(xf[s], O::tokens(sm.p[hw][i], s, g), y);
+            for (int s = 0; s * O::KS < 16 * (ti + 1); ++s) {
+              const F p = O::tokens(sm.p[hw][i], s, g);
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct) y[ct] = O::mma(xf[ct][s], p, y[ct]);
+            }
           } else {
+#pragma unroll 1
             for (int j = 0; j <= i; ++j) {
               const float p = to_f32(sm.p[hw][i][j]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] += p * to_f32(sm.x[j][16 * wave + 4 * g + e]);
+              for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  y[ct][e] += p * to_f32(sm.x[j][lcol + 16 * ct + 4 * g + e]);
             }
           }
-          float xv[4];
-          load_row<T, 4>(&sm.x[i][16 * wave + 4 * g], xv);
-          if (t0 + i < n)
-            store4<T>(static_cast<T*>(a.y) + (static_cast<size_t>(b) * a.T + t0 + i) * xrow +
-                          static_cast<size_t>(head) * a.P + pcol + 4 * g,
-                      y[0] + dskip * xv[0], y[1] + dskip * xv[1], y[2] + dskip * xv[2],
-                      y[3] + dskip * xv[3]);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            float xv[4];
+            load_row<T, 4>(&sm.x[i][lcol + 16 * ct + 4 * g], xv);
+            if (t0 + i < n)
+              store4<T>(reinterpret_cast<T*>(yp + 16 * ti * xrow * sizeof(T) + off_y) + 16 * ct,
+                        y[ct][0] + dskip * xv[0], y[ct][1] + dskip * xv[1],
+                        y[ct][2] + dskip * xv[2], y[ct][3] + dskip * xv[3]);
+          }
+          // One tile row at a time: its operands stay out of the registers of
+          // the next.
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-      const float decay = sm.eg[hw][L - 1];
+      const float decay = w.eg[L - 1];
 #pragma unroll
-      for (int k = 0; k < NTL; ++k) S[k] *= decay;
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int k = 0; k < NTL; ++k) S[ct][k] *= decay;
 #pragma unroll
       for (int s = 0; s < KL; ++s) {
-        F wx[O::PIECES];
-        O::weigh(xf[s], sm.w[hw], s, g, wx);
+        F wx[CT][O::PIECES];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) O::weigh(xf[ct][s], w.w, s, g, wx[ct]);
 #pragma unroll
         for (int k = 0; k < NTL; ++k) {
-          const F bt = O::columns(&sm.b[0][0], Sh::LB, s, g, r, 16 * k);
+          const F bt = O::template columns<EV>(&sm.b[0][0], Sh::LB, s, g, r, 16 * k);
 #pragma unroll
-          for (int q = 0; q < O::PIECES; ++q) S[k] = O::mma(bt, wx[q], S[k]);
+          for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int q = 0; q < O::PIECES; ++q) S[ct][k] = O::mma(bt, wx[ct][q], S[ct][k]);
         }
       }
-      if constexpr (kStates)
-        total += static_cast<double>(sm.gh[hw][L - 1]) + sm.gl[hw][L - 1];
+      if constexpr (kStates) total += static_cast<double>(w.gh[L - 1]) + w.gl[L - 1];
+    }
+    if (chunk + 1 < end) {
+      rows_of(chunk + 1);  // the other half of sm.rows
+      if (chunk + 2 < end) request_dt(chunk + 2);
     }
     __syncthreads();
   }
@@ -444,12 +596,14 @@ __global__ __launch_bounds__(64 * NW) void ssm_chunk_kernel(SsmArgs a, int block
   }
   if (to) {
 #pragma unroll
-    for (int k = 0; k < NTL; ++k)
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = 16 * k + 4 * g + e;
-        if (row < N) to[static_cast<size_t>(row) * a.P + pcol + r] = S[k][e];
-      }
+      for (int k = 0; k < NTL; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 16 * k + 4 * g + e;
+          if (row < N) to[static_cast<size_t>(row) * a.P + pcol + 16 * ct + r] = S[ct][k][e];
+        }
   }
 }
 
@@ -466,28 +620,47 @@ __global__ __launch_bounds__(256) void ssm_start_kernel(SsmArgs a, int segs) {
   float4 s = a.state_in ? reinterpret_cast<const float4*>(a.state_in)[unit * quads + q]
                         : make_float4(0.f, 0.f, 0.f, 0.f);
   starts[0] = s;
-  for (int k = 1; k < segs; ++k) {
-    const float f = __builtin_amdgcn_exp2f(decays[k - 1]);
-    const float4 m = starts[k * quads];
-    s = make_float4(f * s.x + m.x, f * s.y + m.y, f * s.z + m.z, f * s.w + m.w);
-    starts[k * quads] = s;
+  constexpr int kAhead = 8;  // loads in flight: no store of the loop is read by it
+  for (int k0 = 1; k0 < segs; k0 += kAhead) {
+    float4 m[kAhead];
+    float f[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = min(k0 + i, segs - 1);
+      m[i] = starts[k * quads];
+      f[i] = decays[k - 1];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float e = __builtin_amdgcn_exp2f(f[i]);
+      s = make_float4(e * s.x + m[i].x, e * s.y + m[i].y, e * s.z + m[i].z, e * s.w + m[i].w);
+      if (k0 + i < segs) starts[(k0 + i) * quads] = s;
+    }
   }
 }
 
 struct Cut {
+  int cols;        // columns of a workgroup
   int blocks;      // column blocks of a group
   int segs;        // segments of the sequence
   int seg_chunks;  // chunks of a segment
 };
 
-// Columns of a workgroup: 64, or 32 where the P tiles of four 16-wide heads in
-// fp32 would not fit LDS.
-int block_cols(int P, int io_bf16) { return !io_bf16 && P == 16 ? 32 : 64; }
+// Columns of a workgroup.  128 (two tiles a wave): every operand of B, C and P
+// that is read from LDS serves two products, and heads of 64 share G.  64 where
+// the group has no more or a head is narrower than two tiles, and for fp32,
+// whose operands fill LDS; 32 where the P tiles of four 16-wide heads in fp32
+// would not fit.
+int block_cols(int width, int P, int io_bf16) {
+  if (!io_bf16) return P == 16 ? 32 : 64;
+  return width > 64 && P >= 32 ? 128 : 64;
+}
 
 Cut cut_of(int B, int T, int G, int H, int P, int io_bf16) {
   Cut c;
-  const int width = H / G * P, cols = block_cols(P, io_bf16);
-  c.blocks = (width + cols - 1) / cols;
+  const int width = H / G * P;
+  c.cols = block_cols(width, P, io_bf16);
+  c.blocks = (width + c.cols - 1) / c.cols;
   const int chunks = (T + L - 1) / L;
   const long long units = static_cast<long long>(B) * G * c.blocks;
   // Enough workgroups for two on every CU, segments of at least 4 chunks.
@@ -499,29 +672,41 @@ Cut cut_of(int B, int T, int G, int H, int P, int io_bf16) {
   return c;
 }
 
-template <typename T, int N, int HB, int NW>
+template <typename T, int N, int HB, int NW, int CT>
 hipError_t launch_shape(const SsmArgs& a, const Cut& c, hipStream_t stream) {
-  using Sh = Shape<T, N, HB, NW>;
-  static_assert(sizeof(Sh) <= 160 * 1024, "LDS of a workgroup");
+  using Full = Shape<T, N, HB, NW, CT, false>;
+  using States = Shape<T, N, HB, NW, CT, true>;
+  static_assert(sizeof(Full) <= 160 * 1024, "LDS of a workgroup");
   const unsigned units = static_cast<unsigned>(a.B) * a.G * c.blocks;
   if (c.segs > 1) {
-    hipLaunchKernelGGL((ssm_chunk_kernel<T, N, HB, NW, true>), dim3(units * (c.segs - 1)),
-                       dim3(Sh::NT), sizeof(Sh), stream, a, c.blocks, c.segs, c.seg_chunks);
+    hipLaunchKernelGGL((ssm_chunk_kernel<T, N, HB, NW, CT, true>), dim3(units * (c.segs - 1)),
+                       dim3(States::NT), sizeof(States), stream, a, c.blocks, c.segs,
+                       c.seg_chunks);
     const size_t quads = static_cast<size_t>(a.B) * a.H * a.N * a.P / 4;
     hipLaunchKernelGGL(ssm_start_kernel, dim3(static_cast<unsigned>((quads + 255) / 256)),
                        dim3(256), 0, stream, a, c.segs);
   }
-  hipLaunchKernelGGL((ssm_chunk_kernel<T, N, HB, NW, false>), dim3(units * c.segs), dim3(Sh::NT),
-                     sizeof(Sh), stream, a, c.blocks, c.segs, c.seg_chunks);
+  hipLaunchKernelGGL((ssm_chunk_kernel<T, N, HB, NW, CT, false>), dim3(units * c.segs),
+                     dim3(Full::NT), sizeof(Full), stream, a, c.blocks, c.segs, c.seg_chunks);
   return hipGetLastError();
 }
 
 template <typename T, int N>
 hipError_t launch_n(const SsmArgs& a, const Cut& c, hipStream_t stream) {
-  if (a.P >= 64) return launch_shape<T, N, 1, 4>(a, c, stream);
-  if (a.P == 32) return launch_shape<T, N, 2, 4>(a, c, stream);
-  if constexpr (sizeof(T) == 4) return launch_shape<T, N, 2, 2>(a, c, stream);
-  else return launch_shape<T, N, 4, 4>(a, c, stream);
+  if constexpr (sizeof(T) == 4) {
+    if (a.P >= 64) return launch_shape<T, N, 1, 4, 1>(a, c, stream);
+    if (a.P == 32) return launch_shape<T, N, 2, 4, 1>(a, c, stream);
+    return launch_shape<T, N, 2, 2, 1>(a, c, stream);
+  } else {
+    if (c.cols == 128) {
+      if (a.P == 128) return launch_shape<T, N, 1, 4, 2>(a, c, stream);
+      if (a.P == 64) return launch_shape<T, N, 2, 4, 2>(a, c, stream);
+      return launch_shape<T, N, 4, 4, 2>(a, c, stream);
+    }
+    if (a.P >= 64) return launch_shape<T, N, 1, 4, 1>(a, c, stream);
+    if (a.P == 32) return launch_shape<T, N, 2, 4, 1>(a, c, stream);
+    return launch_shape<T, N, 4, 4, 1>(a, c, stream);
+  }
 }
 
 template <typename T>

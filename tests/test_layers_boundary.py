@@ -78,6 +78,8 @@ def ssm(step=False, B=2, T=70, G=2, H=4, N=32, P=64, io=1, x=A[0], b=A[1], c=A[2
     (dict(G=3), "SHAPE"), (dict(N=0), "SHAPE"), (dict(N=48), "UNSUPPORTED"),
     (dict(P=8), "UNSUPPORTED"), (dict(P=256), "UNSUPPORTED"),
     (dict(B=2 ** 20, H=2 ** 10), "SHAPE"),
+    (dict(B=1, H=2 ** 17, P=128), "SHAPE"),     # a chunk's rows past 32-bit offsets
+    (dict(B=1, G=2 ** 20, H=2 ** 20, N=128, P=16), "SHAPE"),
     (dict(x=None), "NULL"), (dict(dt=None), "NULL"), (dict(Al=None), "NULL"),
     (dict(s_out=None), "NULL"), (dict(y=None), "NULL"),
     (dict(x=A[0] + 8), "ALIGN"), (dict(y=A[10] + 4), "ALIGN"), (dict(s_out=A[9] + 8), "ALIGN"),
