@@ -663,10 +663,13 @@ Cut cut_of(int B, int T, int G, int H, int P, int io_bf16) {
   c.blocks = (width + c.cols - 1) / c.cols;
   const int chunks = (T + L - 1) / L;
   const long long units = static_cast<long long>(B) * G * c.blocks;
-  // Enough workgroups for two on every CU, segments of at least 4 chunks.
-  long long segs = (512 + units - 1) / units;
-  if (segs > chunks / 4) segs = chunks / 4;
-  if (segs < 1) segs = 1;
+  // As many workgroups as the GPU holds at a time, two on each of 256 CUs, and
+  // not one more (a second round for a few costs as much as for all); segments
+  // of at least 2 chunks, and none below 6, where the first pass and its
+  // launches cost more than they save.
+  long long segs = 512 / units;
+  if (segs > chunks / 2) segs = chunks / 2;
+  if (segs < 1 || chunks < 6) segs = 1;
   c.seg_chunks = static_cast<int>((chunks + segs - 1) / segs);
   c.segs = c.seg_chunks > 0 ? (chunks + c.seg_chunks - 1) / c.seg_chunks : 1;
   return c;
