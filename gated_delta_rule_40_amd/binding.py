@@ -11,6 +11,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 from pathlib import Path
 
 import torch
@@ -237,21 +238,26 @@ def gdr_prefill_chunked_noalloc(q, k, v, gate_in, beta_logit, state_in, state_ou
 # launch goes to the tensors' device whatever the current one is.
 # ---------------------------------------------------------------------------
 _F8 = (torch.float8_e4m3fn, torch.uint8)
+_F32, _I32 = torch.float32, torch.int32
+_IO = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16}
 
 
 def _ptr(t, name, shape, dtype, device):
     """Device address of a dense tensor of exactly this shape, dtype and device."""
+    try:
+        if (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _opt(t, name, shape, dtype, device):
@@ -259,28 +265,40 @@ def _opt(t, name, shape, dtype, device):
 
 
 def _lead(t, name, dims):
-    """Shape, dtype and device of the tensor that sets the sizes of a call."""
+    """Shape, dtype code and device of the tensor that sets the sizes of a call."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} is on {t.device}, expected a GPU")
-    return t.shape, _io_code(t.dtype), t.device
+    shape, device = t.shape, t.device
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {len(shape)}")
+    if device.type != "cuda":
+        raise ValueError(f"{name} is on {device}, expected a GPU")
+    io = _IO.get(t.dtype)
+    return shape, _io_code(t.dtype) if io is None else io, device
+
+
+def _sized(struct):
+    """Dimension structs by their sizes: a serving loop repeats a few."""
+    return functools.lru_cache(maxsize=256)(struct)
+
+
+_conv_dims, _ssm_dims, _kv_dims = _sized(gdr_conv_dims), _sized(gdr_ssm_dims), _sized(gdr_kv_dims)
+
+# The current stream's handle as an integer: torch's own accessor for it where
+# there is one (0.1 us), else through a Stream object (2 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _launch(name, dev, stream, *args):
     """Calls an entry point with the stream as its last argument, on `dev`."""
-    fn = getattr(load_library(), name)
-    here = torch.cuda.current_device()
-    if dev.index != here:
-        torch.cuda.set_device(dev)
-    try:
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        rc = fn(*args, s.cuda_stream)
-    finally:
-        if dev.index != here:
-            torch.cuda.set_device(here)
+    fn = getattr(_lib or load_library(), name)
+    index, here = dev.index, torch.cuda.current_device()
+    if index == here:
+        rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != GDR_OK:
         raise GdrError(rc, name)
 
@@ -295,10 +313,9 @@ def gdr_conv_step(x, weight, bias, state, y, *, silu=True, stream=None):
     row = C if B <= 1 and x.is_contiguous() else x.stride(0)
     if x.stride(1) != 1 and C > 1:
         raise ValueError("x's channels must be contiguous")
-    f32 = torch.float32
-    _launch("gdr_conv_step", dev, stream, gdr_conv_dims(B, 1, W, C, 0, 0), io, int(bool(silu)),
-            x.data_ptr(), row, _ptr(weight, "weight", (C, W), f32, dev),
-            _opt(bias, "bias", (C,), f32, dev), _ptr(state, "state", (B, W - 1, C), x.dtype, dev),
+    _launch("gdr_conv_step", dev, stream, _conv_dims(B, 1, W, C, 0, 0), io, int(bool(silu)),
+            x.data_ptr(), row, _ptr(weight, "weight", (C, W), _F32, dev),
+            _opt(bias, "bias", (C,), _F32, dev), _ptr(state, "state", (B, W - 1, C), x.dtype, dev),
             _ptr(y, "y", (B, C), x.dtype, dev))
 
 
@@ -324,10 +341,10 @@ def gdr_conv_prefill(x, weight, bias, state_in, state_out, outs, *, silu=True, l
     ys = [_ptr(o, f"outs[{i}]", (B, T, c[i]), x.dtype, dev) for i, o in enumerate(outs)]
     c += [0] * (3 - len(c))
     ys += [None] * (3 - len(ys))
-    f32, st = torch.float32, (B, W - 1, C)
-    _launch("gdr_conv_prefill", dev, stream, gdr_conv_dims(B, T, W, *c), io, int(bool(silu)),
-            x.data_ptr(), row, _ptr(weight, "weight", (C, W), f32, dev),
-            _opt(bias, "bias", (C,), f32, dev), _opt(lens, "lens", (B,), torch.int32, dev),
+    st = (B, W - 1, C)
+    _launch("gdr_conv_prefill", dev, stream, _conv_dims(B, T, W, *c), io, int(bool(silu)),
+            x.data_ptr(), row, _ptr(weight, "weight", (C, W), _F32, dev),
+            _opt(bias, "bias", (C,), _F32, dev), _opt(lens, "lens", (B,), _I32, dev),
             _opt(state_in, "state_in", st, x.dtype, dev),
             _ptr(state_out, "state_out", st, x.dtype, dev), *ys)
 
@@ -337,16 +354,15 @@ def gdr_ssm_step(xbc, dt, A_log, dt_bias, D, state, y, *, G, H, N, P, stream=Non
     (float32 or bfloat16), dt [B,H] fp32, A_log [H], dt_bias and D [H] or None,
     state [B,H,N,P] fp32 (updated in place), y [B,H,P] in xbc's dtype."""
     (B, width), io, dev = _lead(xbc, "xbc", 2)
-    f32 = torch.float32
-    _launch("gdr_ssm_step", dev, stream, gdr_ssm_dims(B, 1, G, H, N, P), io,
+    _launch("gdr_ssm_step", dev, stream, _ssm_dims(B, 1, G, H, N, P), io,
             _ptr(xbc, "xbc", (B, H * P + 2 * G * N), xbc.dtype, dev),
-            _ptr(dt, "dt", (B, H), f32, dev), _ptr(A_log, "A_log", (H,), f32, dev),
-            _opt(dt_bias, "dt_bias", (H,), f32, dev), _opt(D, "D", (H,), f32, dev),
-            _ptr(state, "state", (B, H, N, P), f32, dev), _ptr(y, "y", (B, H, P), xbc.dtype, dev))
+            _ptr(dt, "dt", (B, H), _F32, dev), _ptr(A_log, "A_log", (H,), _F32, dev),
+            _opt(dt_bias, "dt_bias", (H,), _F32, dev), _opt(D, "D", (H,), _F32, dev),
+            _ptr(state, "state", (B, H, N, P), _F32, dev), _ptr(y, "y", (B, H, P), xbc.dtype, dev))
 
 
 def gdr_ssm_workspace_size(B, T, G, H, N, P, io_dtype) -> int:
-    return int(load_library().gdr_ssm_workspace_size(gdr_ssm_dims(B, T, G, H, N, P),
+    return int(load_library().gdr_ssm_workspace_size(_ssm_dims(B, T, G, H, N, P),
                                                      _io_code(io_dtype)))
 
 
@@ -375,14 +391,14 @@ def gdr_ssm_prefill(x, b, c, dt, A_log, dt_bias, D, state_in, state_out, y, work
         flat = isinstance(t, torch.Tensor) and t.dim() == 3
         return _ptr(t, name, (B, T, heads * width) if flat else (B, T, heads, width), x.dtype, dev)
 
-    f32, st = torch.float32, (B, H, N, P)
+    st = (B, H, N, P)
     ws, ws_bytes = _space(workspace, dev)
-    _launch("gdr_ssm_prefill", dev, stream, gdr_ssm_dims(B, T, G, H, N, P), io,
+    _launch("gdr_ssm_prefill", dev, stream, _ssm_dims(B, T, G, H, N, P), io,
             rows(x, "x", H, P), rows(b, "b", G, N), rows(c, "c", G, N),
-            _ptr(dt, "dt", (B, T, H), f32, dev), _ptr(A_log, "A_log", (H,), f32, dev),
-            _opt(dt_bias, "dt_bias", (H,), f32, dev), _opt(D, "D", (H,), f32, dev),
-            _opt(lens, "lens", (B,), torch.int32, dev), _opt(state_in, "state_in", st, f32, dev),
-            _ptr(state_out, "state_out", st, f32, dev), rows(y, "y", H, P), ws, ws_bytes)
+            _ptr(dt, "dt", (B, T, H), _F32, dev), _ptr(A_log, "A_log", (H,), _F32, dev),
+            _opt(dt_bias, "dt_bias", (H,), _F32, dev), _opt(D, "D", (H,), _F32, dev),
+            _opt(lens, "lens", (B,), _I32, dev), _opt(state_in, "state_in", st, _F32, dev),
+            _ptr(state_out, "state_out", st, _F32, dev), rows(y, "y", H, P), ws, ws_bytes)
 
 
 def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table, pos, lens, B, H_kv, D, dev):
@@ -394,14 +410,14 @@ def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table, pos, lens, B, H
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a tensor [B,max_pages]")
     n_pages, page, per = k_cache.shape[0], k_cache.shape[2], block_table.shape[1]
-    f8, f32, i32 = k_cache.dtype, torch.float32, torch.int32
+    f8 = k_cache.dtype
     return (page, n_pages, per), (
         _ptr(k_cache, "k_cache", (n_pages, H_kv, page, D), f8, dev),
         _ptr(v_cache, "v_cache", (n_pages, H_kv, D, page), f8, dev),
-        _ptr(k_scale, "k_scale", (n_pages, H_kv), f32, dev),
-        _ptr(v_scale, "v_scale", (n_pages, H_kv), f32, dev),
-        _ptr(block_table, "block_table", (B, per), i32, dev), _ptr(pos, "pos", (B,), i32, dev),
-        _opt(lens, "lens", (B,), i32, dev))
+        _ptr(k_scale, "k_scale", (n_pages, H_kv), _F32, dev),
+        _ptr(v_scale, "v_scale", (n_pages, H_kv), _F32, dev),
+        _ptr(block_table, "block_table", (B, per), _I32, dev), _ptr(pos, "pos", (B,), _I32, dev),
+        _opt(lens, "lens", (B,), _I32, dev))
 
 
 def gdr_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, pos, *, lens=None,
@@ -413,14 +429,14 @@ def gdr_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, pos, *,
     (B, T, H_kv, D), io, dev = _lead(k, "k", 4)
     sizes, (kc, vc, ks, vs, bt, ps, ln) = _cache_args(k_cache, v_cache, k_scale, v_scale,
                                                       block_table, pos, lens, B, H_kv, D, dev)
-    _launch("gdr_kv_append", dev, stream, gdr_kv_dims(B, T, 0, H_kv, D, *sizes), io,
+    _launch("gdr_kv_append", dev, stream, _kv_dims(B, T, 0, H_kv, D, *sizes), io,
             _ptr(k, "k", (B, T, H_kv, D), k.dtype, dev), _ptr(v, "v", (B, T, H_kv, D), k.dtype, dev),
             bt, ps, ln, kc, vc, ks, vs)
 
 
 def gdr_attn_workspace_size(B, T, H_q, H_kv, D, page, max_pages, io_dtype) -> int:
     return int(load_library().gdr_attn_workspace_size(
-        gdr_kv_dims(B, T, H_q, H_kv, D, page, 0, max_pages), _io_code(io_dtype)))
+        _kv_dims(B, T, H_q, H_kv, D, page, 0, max_pages), _io_code(io_dtype)))
 
 
 def gdr_attn_cached(q, k_cache, v_cache, k_scale, v_scale, block_table, pos, o, workspace=None, *,
@@ -434,6 +450,6 @@ def gdr_attn_cached(q, k_cache, v_cache, k_scale, v_scale, block_table, pos, o, 
     sizes, (kc, vc, ks, vs, bt, ps, ln) = _cache_args(k_cache, v_cache, k_scale, v_scale,
                                                       block_table, pos, lens, B, H_kv, D, dev)
     ws, ws_bytes = _space(workspace, dev)
-    _launch("gdr_attn_cached", dev, stream, gdr_kv_dims(B, T, H_q, H_kv, D, *sizes), io,
+    _launch("gdr_attn_cached", dev, stream, _kv_dims(B, T, H_q, H_kv, D, *sizes), io,
             _ptr(q, "q", (B, T, H_q, D), q.dtype, dev), kc, vc, ks, vs, bt, ps, ln,
             _ptr(o, "o", (B, T, H_q, D), q.dtype, dev), float(scale), ws, ws_bytes)

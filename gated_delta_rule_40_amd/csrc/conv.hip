@@ -5,12 +5,16 @@
 //
 // where u_t = x_t for t >= 0 and the state's rows before that.
 //
-// A thread owns VEC neighbouring channels (16 bytes of a row) over kTile
+// A thread owns VEC neighbouring channels (16 bytes of a row) over TILE
 // consecutive tokens and slides the W-token window down them in registers, so
 // every input is read once but for the W - 1 rows before a tile; weights and
 // bias stay in registers over the tile.  Bound by HBM: a value costs one read
 // and one write, and about 17 issue slots, which is why the sigmoid goes
-// through the hardware exp2 and reciprocal.
+// through the hardware exp2 and reciprocal.  8192 channels in bf16: 4000 tokens
+// 34.5 us (131 MB, 3.8 TB/s), 500 tokens 8.7 us, 64 single tokens 5.8 us.
+// Stores past the caches would take 26.8 us for the 4000 tokens, but the scan
+// that reads the outputs next then takes 11 us more: the two together are
+// faster with plain stores at every length (4000 tokens 104 against 108 us).
 //
 // The thread of a row's first tile also writes the new state: it alone reads
 // the old one, so the state may be updated in place.
@@ -22,7 +26,10 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 16;  // tokens per thread
+// Threads that a prompt's tiles should give.  With 8192 channels, tiles of 32
+// against 16 tokens: 500 tokens (16 or 32 thousand threads) 12.4 against 8.8 us,
+// 1500 tokens (48 or 96 thousand) 14.6 against 15.4 us.
+constexpr long long kFill = 40000;
 
 template <typename T, int VEC>
 struct Pack {
@@ -53,7 +60,8 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<T, VEC>& r) {
   }
 }
 
-template <typename T, int VEC, int W, bool SILU>
+// TILE: tokens per thread (1 for single tokens).
+template <typename T, int VEC, int W, bool SILU, int TILE>
 __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int tiles, int groups) {
   const unsigned idx = blockIdx.x * kThreads + threadIdx.x;
   const unsigned cg = idx % groups;
@@ -62,7 +70,7 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int tiles, i
   const int b = bt / tiles;
   if (b >= a.B) return;
   const int n = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
-  const int t0 = tile * kTile;
+  const int t0 = tile * TILE;
   if (t0 >= n && tile > 0) return;
   const int c = cg * VEC;
 
@@ -138,8 +146,8 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int tiles, i
 #pragma unroll
     for (int e = 0; e < VEC; ++e) u[w][e] = to_f32(win[w].e[e]);
 
-  constexpr int kAhead = 8;  // rows requested together
-  for (int tb = t0; tb < min(t0 + kTile, n); tb += kAhead) {
+  constexpr int kAhead = TILE < 8 ? TILE : 8;  // rows requested together
+  for (int tb = t0; tb < min(t0 + TILE, n); tb += kAhead) {
     P in[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
@@ -162,19 +170,31 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a, int tiles, i
   }
 }
 
-template <typename T, int VEC, int W>
-hipError_t launch_w(const ConvArgs& a, hipStream_t stream) {
+template <typename T, int VEC, int W, int TILE>
+hipError_t launch_tile(const ConvArgs& a, hipStream_t stream) {
   const int groups = a.C / VEC;
-  const int tiles = a.T > kTile ? (a.T + kTile - 1) / kTile : 1;
+  const int tiles = a.T > TILE ? (a.T + TILE - 1) / TILE : 1;
   const long long threads = static_cast<long long>(groups) * tiles * a.B;
   const dim3 grid(static_cast<unsigned>((threads + kThreads - 1) / kThreads));
   if (a.silu)
-    hipLaunchKernelGGL((conv_kernel<T, VEC, W, true>), grid, dim3(kThreads), 0, stream, a, tiles,
-                       groups);
+    hipLaunchKernelGGL((conv_kernel<T, VEC, W, true, TILE>), grid, dim3(kThreads), 0, stream, a,
+                       tiles, groups);
   else
-    hipLaunchKernelGGL((conv_kernel<T, VEC, W, false>), grid, dim3(kThreads), 0, stream, a, tiles,
-                       groups);
+    hipLaunchKernelGGL((conv_kernel<T, VEC, W, false, TILE>), grid, dim3(kThreads), 0, stream, a,
+                       tiles, groups);
   return hipGetLastError();
+}
+
+template <typename T, int VEC, int W>
+hipError_t launch_w(const ConvArgs& a, hipStream_t stream) {
+  if (a.T <= 1) return launch_tile<T, VEC, W, 1>(a, stream);
+  // The longest tile (fewest rows read twice) that still gives kFill threads.
+  const long long columns = static_cast<long long>(a.C / VEC) * a.B;
+  auto fills = [&](int tile) { return columns * ((a.T + tile - 1) / tile) >= kFill; };
+  if (fills(32)) return launch_tile<T, VEC, W, 32>(a, stream);
+  if (fills(16)) return launch_tile<T, VEC, W, 16>(a, stream);
+  if (fills(8)) return launch_tile<T, VEC, W, 8>(a, stream);
+  return launch_tile<T, VEC, W, 4>(a, stream);
 }
 
 template <typename T, int VEC>
@@ -199,7 +219,7 @@ hipError_t launch_io(const ConvArgs& a, hipStream_t stream) {
 }  // namespace
 
 long long conv_max_grid(int B, int T, int C) {
-  const long long tiles = T > kTile ? (static_cast<long long>(T) + kTile - 1) / kTile : 1;
+  const long long tiles = T > 4 ? (static_cast<long long>(T) + 3) / 4 : 1;
   // Each factor is below 2^31; the product of the first two is checked before
   // the third can overflow 64 bits.
   const long long rows = tiles * B;

@@ -156,6 +156,29 @@ def test_steps(B, G, H, N, P, io):
         check(d, s0, (torch.stack(ys, 1), S.cpu()))
 
 
+def test_step_of_a_large_state():
+    """A state of 72 MiB (it passes the caches by): rows against the same rows alone."""
+    require_gpu()
+    announce("ssm step B=72 H=32 N=128 P=64")
+    B, G, H, N, P = 72, 4, 32, 128, 64
+    d, s0 = inputs(3, B, 1, G, H, N, P, "bf16")
+    g, S = up(d), s0.to(DEV)
+    xbc = torch.cat([g[k][:, 0].flatten(1) for k in ("x", "b", "c")], 1).contiguous()
+    y = torch.empty((B, H, P), dtype=g["x"].dtype, device=DEV)
+    size = dict(G=G, H=H, N=N, P=P)
+    dt = g["dt"][:, 0].contiguous()
+    for rows in (slice(0, 5), slice(67, 72)):
+        part, yp = s0[rows].to(DEV), torch.empty_like(y[rows])
+        gdr.gdr_ssm_step(xbc[rows], dt[rows], g["A_log"], g["dt_bias"], g["D"], part, yp, **size)
+        whole = S.clone()
+        gdr.gdr_ssm_step(xbc, dt, g["A_log"], g["dt_bias"], g["D"], whole, y, **size)
+        assert torch.equal(whole[rows], part) and torch.equal(y[rows], yp)
+    want, mag, st, M = ref.ssm(**d, state=s0)
+    assert ref.worst(y.cpu(), want[:, 0], 2.0 ** -8 * want[:, 0].abs()
+                     + ref.ssm_units(1, N) * EPS * mag[:, 0]) <= 1
+    assert ref.worst(whole.cpu(), st, ref.ssm_units(1, N) * EPS * M + 1e-30) <= 1
+
+
 def test_no_tokens_copies_the_state():
     require_gpu()
     announce("ssm T=0 and B=0")
