@@ -61,7 +61,7 @@ def append(c, k, v, pos, lens=None, dev=None):
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("Hkv,D,page", [(1, 64, 16), (2, 128, 64), (3, 64, 128), (5, 128, 32)])
-@pytest.mark.parametrize("T", [1, 2, 15, 33, 130])
+@pytest.mark.parametrize("T", [1, 2, 8, 15, 33, 130])
 def test_append(T, Hkv, D, page, io):
     require_gpu()
     announce(f"append T={T} Hkv={Hkv} D={D} page={page} io={io}")
