@@ -22,13 +22,16 @@
 // e4m3 values are exact in bf16.  The key scales join the score scale, the
 // value scales (powers of two) multiply p.  p itself is split into bf16
 // pieces: two for bf16 io (2^-17 of it is lost, far below the output's own
-// rounding), three, like q, for fp32 io (2^-25).
+// rounding; one in attn_rows_kernel, where the second product is half the work:
+// a second rounding of the output's size), three, like q, for fp32 io (2^-25).
 //
-// Bound by HBM for few query rows (one byte a cached element), by the matrix
-// and conversion pipes for prompts.  With few rows the waves of a workgroup
-// share the keys and join in LDS (kShare); with many each takes its own rows.
-// Where that gives too few workgroups, the keys are also cut into splits over
-// workgroups, whose partial sums attn_join_kernel joins.
+// Two kernels.  With few query rows (attn_few_kernel, the order above) the
+// waves of a workgroup share the keys and join in LDS: bound by HBM, one byte a
+// cached element.  With many (attn_rows_kernel) each wave takes its own rows,
+// the workgroup's waves read the same keys, and a step's keys and values are
+// converted once, with their scales, into LDS: bound by the matrix and
+// exponential pipes.  Where that gives too few workgroups, the keys are also
+// cut into splits over workgroups, whose partial sums attn_join_kernel joins.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -41,18 +44,23 @@ namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
+// Query rows of a workgroup of attn_rows_kernel.
+template <int MT>
+constexpr int kRowsBlock = 16 * MT * (kThreads / 64);
 constexpr int kTile = 64;  // keys per step
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// Eight e4m3 codes as bf16 (exact).
-__device__ __forceinline__ bf16x8_t codes_to_bf16(unsigned w0, unsigned w1) {
-  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
-  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
-  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
-  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
+// Eight e4m3 codes as bf16, times a power of two (exact).
+__device__ __forceinline__ bf16x8_t codes_to_bf16(unsigned w0, unsigned w1, float scale = 1.0f) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, true);
   return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
@@ -118,14 +126,14 @@ __device__ __forceinline__ Partial partial_of(const KvArgs& a, int splits, size_
   return {base + row * splits * a.D, base + rows * splits * a.D + row * splits * 2};
 }
 
-template <typename T, int D, int MT, bool kShare>
-__global__ __launch_bounds__(kThreads) void attn_kernel(KvArgs a, int row_blocks, int splits) {
+template <typename T, int D, int NW>
+__global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blocks, int splits) {
   constexpr int QP = sizeof(T) == 4 ? 3 : 1;  // pieces of q
   constexpr int PP = sizeof(T) == 4 ? 3 : 2;  // pieces of p
   constexpr int KS = D / 32;                  // contraction steps of S^T
   constexpr int KW = D / 64;                  // 16-byte loads of a lane's key slice
   constexpr int DT = D / 16;                  // row tiles of O^T
-  constexpr int kWaves = kThreads / 64;
+  constexpr int MT = 1;                       // tiles of query rows
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
 
@@ -137,16 +145,15 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(KvArgs a, int row_blocks
   const int block = row_blocks - 1 - rest / splits;  // longest first
   const int group = a.H_q / a.H_kv;
   const int n = tokens_of(a, b);
-  const int row0 = (kShare ? block : block * kWaves + wave) * 16 * MT;
+  const int row0 = block * 16;
   if (row0 >= n * group) return;
-  const int last = min(row0 + 16 * MT, n * group) - 1;
+  const int last = min(row0 + 16, n * group) - 1;
   const Span span{key_limit(a, b, row0 / group), key_limit(a, b, last / group)};
 
   const int steps = (span.hi + kTile - 1) / kTile;
   const int per = split_steps(steps, splits);
   const int s_end = min((part + 1) * per, steps);
-  constexpr int kStride = kShare ? kWaves : 1;
-  int step = part * per + (kShare ? wave : 0);
+  int step = part * per + wave;
   if (splits > 1 && part * per >= steps && part > 0) return;  // not read by the join
 
   // This lane's query rows: one per tile, column r.
@@ -221,12 +228,12 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(KvArgs a, int row_blocks
     idv = page_of(step, g);
     load_k(step, idk);
   }
-  for (; step < s_end; step += kStride) {
+  for (; step < s_end; step += NW) {
     load_v(step, idv);
     const size_t ph = static_cast<size_t>(max(idv, 0)) * a.H_kv + head;
     const float ks = a.k_scale[ph] * (a.scale * kLog2e);
     float vs = a.v_scale[ph];
-    const int next = step + kStride;
+    const int next = step + NW;
     int idk2 = -1, idv2 = -1;
     if (next < s_end) {
       idk2 = page_of(next, ka);
@@ -353,80 +360,339 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(KvArgs a, int row_blocks
     sum[m] += __shfl_xor(sum[m], 32, 64);
   }
 
-  if constexpr (kShare) {
-    // Join the waves' sums: every wave leaves its own in LDS, then 16 threads
-    // share a row.
-    static_assert(MT == 1, "one tile of rows");
+  // Join the waves' sums: every wave leaves its own in LDS, then 16 threads
+  // share a row.
     constexpr int LD = D + 4;
-    __shared__ float acc_s[kWaves][16][LD], ml_s[kWaves][16][2];
+  __shared__ float acc_s[NW][16][LD], ml_s[NW][16][2];
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
-      *reinterpret_cast<f32x4*>(&acc_s[wave][r][16 * d + 4 * g]) = acc[0][d];
-    if (g == 0) {
-      ml_s[wave][r][0] = mx[0];
-      ml_s[wave][r][1] = sum[0];
-    }
-    __syncthreads();
-    const int row = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * (D / 16);
-    if (row0 + row > last) return;
-    float top = -INFINITY, tot = 0.0f, out[D / 16] = {};
+  for (int d = 0; d < DT; ++d)
+    *reinterpret_cast<f32x4*>(&acc_s[wave][r][16 * d + 4 * g]) = acc[0][d];
+  if (g == 0) {
+    ml_s[wave][r][0] = mx[0];
+    ml_s[wave][r][1] = sum[0];
+  }
+  __syncthreads();
+  // Threads past the first 256 have no part in it.
+  const int row = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * (D / 16);
+  if (row >= 16 || row0 + row > last) return;
+  float top = -INFINITY, tot = 0.0f, out[D / 16] = {};
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, ml_s[w][row][0]);
-    const float ref = top == -INFINITY ? 0.0f : top;
+  for (int w = 0; w < NW; ++w) top = fmaxf(top, ml_s[w][row][0]);
+  const float ref = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = __builtin_amdgcn_exp2f(ml_s[w][row][0] - ref);
-      tot += f * ml_s[w][row][1];
+  for (int w = 0; w < NW; ++w) {
+    const float f = __builtin_amdgcn_exp2f(ml_s[w][row][0] - ref);
+    tot += f * ml_s[w][row][1];
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) out[i] += f * acc_s[w][row][c0 + i];
-    }
-    const int qrow = row0 + row;
-    const size_t at =
-        (static_cast<size_t>(b) * a.T + qrow / group) * a.H_q + head * group + qrow % group;
-    if (splits > 1) {
-      const Partial p = partial_of(a, splits, at);
-#pragma unroll
-      for (int i = 0; i < D / 16; i += 4)
-        store4<float>(p.acc + part * D + c0 + i, out[i], out[i + 1], out[i + 2], out[i + 3]);
-      if (c0 == 0) {
-        p.ml[2 * part] = top;
-        p.ml[2 * part + 1] = tot;
-      }
-      return;
-    }
-    const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;  // NaN stays
+    for (int i = 0; i < D / 16; ++i) out[i] += f * acc_s[w][row][c0 + i];
+  }
+  const int qrow = row0 + row;
+  const size_t at =
+      (static_cast<size_t>(b) * a.T + qrow / group) * a.H_q + head * group + qrow % group;
+  if (splits > 1) {
+    const Partial p = partial_of(a, splits, at);
 #pragma unroll
     for (int i = 0; i < D / 16; i += 4)
-      store4<T>(static_cast<T*>(a.o) + at * D + c0 + i, out[i] * inv, out[i + 1] * inv,
-                out[i + 2] * inv, out[i + 3] * inv);
-  } else {
+      store4<float>(p.acc + part * D + c0 + i, out[i], out[i + 1], out[i + 2], out[i + 3]);
+    if (c0 == 0) {
+      p.ml[2 * part] = top;
+      p.ml[2 * part + 1] = tot;
+    }
+    return;
+  }
+  const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;  // NaN stays
+#pragma unroll
+  for (int i = 0; i < D / 16; i += 4)
+    store4<T>(static_cast<T*>(a.o) + at * D + c0 + i, out[i] * inv, out[i + 1] * inv,
+              out[i + 2] * inv, out[i + 3] * inv);
+}
+
+// A step's keys and values in LDS, in bf16 with their scales: keys as rows of D
+// channels; values as rows (channels) of 64 tokens, each 32 tokens in the order
+// in which a lane group takes 8 of them (4 g ... and 16 + 4 g ...).  The pitches
+// keep 16-byte reads of 16 rows on distinct banks.
+template <int D>
+struct Tile {
+  bf16 k[kTile][D + 8];
+  bf16 v[D][kTile + 8];
+};
+
+// MT tiles of 16 query rows a wave, four waves.
+template <typename T, int D, int MT>
+__global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int row_blocks,
+                                                                int splits) {
+  constexpr int QP = sizeof(T) == 4 ? 3 : 1;
+  constexpr int PP = sizeof(T) == 4 ? 3 : 1;
+  constexpr int KS = D / 32, DT = D / 16;
+  constexpr int LW = D / 64;  // 16-byte loads of a thread, of keys and of values
+  __shared__ __attribute__((aligned(16))) Tile<D> tiles[2];
+  __shared__ __attribute__((aligned(16))) int groups_on[2][kThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+
+  const int bh = blockIdx.x % (a.B * a.H_kv);
+  const int rest = blockIdx.x / (a.B * a.H_kv);
+  const int b = bh / a.H_kv, head = bh % a.H_kv;
+  const int part = rest % splits;
+  const int block = row_blocks - 1 - rest / splits;  // longest first
+  const int group = a.H_q / a.H_kv;
+  const int n = tokens_of(a, b);
+  const int block0 = block * kRowsBlock<MT>;
+  if (block0 >= n * group) return;
+  const int block_last = min(block0 + kRowsBlock<MT>, n * group) - 1;
+  const Span all{key_limit(a, b, block0 / group), key_limit(a, b, block_last / group)};
+  const int steps = (all.hi + kTile - 1) / kTile;
+  const int per = split_steps(steps, splits);
+  const int s_end = min((part + 1) * per, steps);
+  int step = part * per;
+  if (step >= steps && part > 0) return;  // not read by the join
+
+  // The wave's rows: one column of S^T a lane and tile.
+  const int row0 = block0 + wave * 16 * MT;
+  const int last = min(row0 + 16 * MT - 1, block_last);
+  const Span span{row0 <= last ? key_limit(a, b, row0 / group) : 0,
+                  row0 <= last ? key_limit(a, b, last / group) : 0};
+  // exp2(c z - c m): c >= 0, the sign of the score scale goes to q; c = 0 would
+  // lose masked keys' -inf.
+  const float c = fmaxf(__builtin_fabsf(a.scale) * kLog2e, 1e-30f);
+  int lim[MT];
+  size_t orow[MT];
+  bf16x8_t q[MT][QP][KS];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = row0 + 16 * m + r;
+    const bool on = row <= last;
+    const int t = on ? row / group : 0;
+    lim[m] = on ? key_limit(a, b, t) : 0;
+    orow[m] = (static_cast<size_t>(b) * a.T + t) * a.H_q + head * group + (on ? row % group : 0);
+    const T* src = static_cast<const T*>(a.q) + orow[m] * D + 8 * g;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      float x[8];
+      load_row<T, 8>(src + 32 * s, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        bf16 p[QP];
+        split<QP>(a.scale < 0.0f ? -x[i] : x[i], p);
+#pragma unroll
+        for (int k = 0; k < QP; ++k) q[m][k][s][i] = p[k];
+      }
+    }
+  }
+
+  // Staging: thread tid loads channels kc ... + 16 LW - 1 of the step's key kt,
+  // and LW groups of 16 tokens of value channel vd.
+  const int* table = a.block_table + static_cast<size_t>(b) * a.max_pages;
+  const int page_shift = __builtin_ctz(a.page);
+  auto page_of = [&](int key) {
+    const int at = key >> page_shift;
+    const int id = at < a.max_pages ? table[at] : -1;
+    return id >= 0 && id < a.n_pages ? id : -1;
+  };
+  const int kt = tid >> 2, kc = (tid & 3) * 16 * LW;
+  const int vd = tid * LW / 4, vt = tid * LW % 4;  // channel, first group of 16 tokens
+  int kid = -1, kid_now = -1, vid[LW];
+  auto find = [&](int s) {
+    kid = page_of(s * kTile + kt);
+#pragma unroll
+    for (int i = 0; i < LW; ++i) vid[i] = page_of(s * kTile + 16 * (vt + i));
+  };
+  u32x4 kr[LW], vr[LW];
+  float ksc, vsc[LW];
+  auto request = [&](int s) {
+    kid_now = kid;
+    const size_t kh = static_cast<size_t>(max(kid, 0)) * a.H_kv + head;
+    const uint8_t* kp = a.k_cache + (kh * a.page + ((s * kTile + kt) & (a.page - 1))) * D + kc;
+    ksc = a.k_scale[kh];
+#pragma unroll
+    for (int i = 0; i < LW; ++i) {
+      kr[i] = *reinterpret_cast<const u32x4*>(kp + 16 * i);
+      const int key = s * kTile + 16 * (vt + i);
+      const size_t vh = static_cast<size_t>(max(vid[i], 0)) * a.H_kv + head;
+      vr[i] = *reinterpret_cast<const u32x4*>(a.v_cache + (vh * D + vd) * a.page +
+                                              (key & (a.page - 1)));
+      // Codes behind the last key, or of no page, count as zeros.
+      const int keep = vid[i] >= 0 ? min(max(all.hi - key, 0), 16) : 0;
+      vsc[i] = keep > 0 ? a.v_scale[vh] : 1.0f;
+      if (keep < 16) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int bytes = min(max(keep - 4 * k, 0), 4);
+          if (bytes < 4) vr[i][k] &= (1u << (8 * bytes)) - 1;
+        }
+      }
+    }
+  };
+
+  f32x4 acc[MT][DT];
+  float mx[MT], sum[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    mx[m] = -INFINITY;
+    sum[m] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  if (step < s_end) {
+    find(step);
+    request(step);
+    if (step + 1 < s_end) find(step + 1);
+  }
+#pragma unroll 1
+  for (; step < s_end; ++step) {
+    Tile<D>& tile = tiles[step & 1];
+    bool odd = false;  // NaN among the values of a step that some rows see in part
+    const bool block_whole = (step + 1) * kTile <= all.lo;
+#pragma unroll
+    for (int i = 0; i < LW; ++i) {
+      *reinterpret_cast<bf16x8_t*>(&tile.k[kt][kc + 16 * i]) = codes_to_bf16(kr[i][0], kr[i][1], ksc);
+      *reinterpret_cast<bf16x8_t*>(&tile.k[kt][kc + 16 * i + 8]) =
+          codes_to_bf16(kr[i][2], kr[i][3], ksc);
+      const bf16x8_t v0 = codes_to_bf16(vr[i][0], vr[i][1], vsc[i]);
+      const bf16x8_t v1 = codes_to_bf16(vr[i][2], vr[i][3], vsc[i]);
+      bf16* vp = &tile.v[vd][32 * ((vt + i) / 2) + 4 * ((vt + i) & 1)];
+      *reinterpret_cast<bf16x4_t*>(vp) = bf16x4_t{v0[0], v0[1], v0[2], v0[3]};
+      *reinterpret_cast<bf16x4_t*>(vp + 8) = bf16x4_t{v0[4], v0[5], v0[6], v0[7]};
+      *reinterpret_cast<bf16x4_t*>(vp + 16) = bf16x4_t{v1[0], v1[1], v1[2], v1[3]};
+      *reinterpret_cast<bf16x4_t*>(vp + 24) = bf16x4_t{v1[4], v1[5], v1[6], v1[7]};
+      if (!block_whole)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) odd |= without_nan(vr[i][k]) != vr[i][k];
+    }
+    // A wave loads 16 neighbouring keys, all of one page: whether there is one.
+    if (lane == 0) groups_on[step & 1][wave] = kid_now >= 0;
+    bool has_nan = false;
+    if (block_whole)
+      __syncthreads();
+    else
+      has_nan = __syncthreads_or(odd);
+    if (step + 1 < s_end) {
+      request(step + 1);
+      if (step + 2 < s_end) find(step + 2);
+    }
+    if (step * kTile >= span.hi) continue;  // nothing here for this wave's rows
+
+    f32x4 z[MT][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) z[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(&tile.k[16 * t + r][32 * s + 8 * g]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int p = 0; p < QP; ++p)
+            z[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[m][p][s], z[m][t], 0, 0, 0);
+      }
+    }
+    const int4 on = *reinterpret_cast<const int4*>(groups_on[step & 1]);
+    const bool whole = (step + 1) * kTile <= span.lo && (on.x & on.y & on.z & on.w);
+    if (!whole) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const bool there = t == 0 ? on.x : t == 1 ? on.y : t == 2 ? on.z : on.w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!(there && step * kTile + 16 * t + 4 * g + e < lim[m])) z[m][t][e] = -INFINITY;
+        }
+    }
+    bf16x8_t p[MT][2][PP];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if (row0 + 16 * m + r > last) continue;
-      if (splits > 1) {
-        const Partial p = partial_of(a, splits, orow[m]);
+      float top = -INFINITY;
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-          store4<float>(p.acc + part * D + 16 * d + 4 * g, acc[m][d][0], acc[m][d][1],
-                        acc[m][d][2], acc[m][d][3]);
-        if (g == 0) {
-          p.ml[2 * part] = mx[m];
-          p.ml[2 * part + 1] = sum[m];
-        }
-        continue;
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, z[m][t][e]);
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      const float now = fmaxf(mx[m], top);
+      const float ref = now == -INFINITY ? 0.0f : now * c;
+      if (__any(now > mx[m])) {
+        const float back = __builtin_amdgcn_exp2f(__builtin_fmaf(mx[m], c, -ref));
+        sum[m] *= back;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[m][d] *= back;
+        mx[m] = now;
       }
-      const float inv = sum[m] == 0.0f ? 0.0f : 1.0f / sum[m];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(z[m][t][e], c, -ref));
+          sum[m] += x;
+          bf16 piece[PP];
+          split<PP>(x, piece);
+#pragma unroll
+          for (int k = 0; k < PP; ++k) p[m][t / 2][k][4 * (t & 1) + e] = piece[k];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        bf16x8_t v = *reinterpret_cast<const bf16x8_t*>(&tile.v[16 * d + r][32 * u + 8 * g]);
+        if (has_nan && !whole) {
+          // NaN of keys that only some rows see: out of the product, and into
+          // the rows that see it.
+          bf16x8_t bad;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const bool is = !(v[i] == v[i]);
+            bad[i] = static_cast<bf16>(is ? 1.0f : 0.0f);
+            if (is) v[i] = static_cast<bf16>(0.0f);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                bad, p[m][u][0], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (hit[e] > 0.0f) acc[m][d][e] = NAN;
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int k = 0; k < PP; ++k)
+            acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[m][u][k], acc[m][d], 0, 0, 0);
+      }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    sum[m] += __shfl_xor(sum[m], 16, 64);
+    sum[m] += __shfl_xor(sum[m], 32, 64);
+    if (row0 + 16 * m + r > last) continue;
+    if (splits > 1) {
+      const Partial o = partial_of(a, splits, orow[m]);
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        store4<T>(static_cast<T*>(a.o) + orow[m] * D + 16 * d + 4 * g, acc[m][d][0] * inv,
-                  acc[m][d][1] * inv, acc[m][d][2] * inv, acc[m][d][3] * inv);
+        store4<float>(o.acc + part * D + 16 * d + 4 * g, acc[m][d][0], acc[m][d][1], acc[m][d][2],
+                      acc[m][d][3]);
+      if (g == 0) {
+        o.ml[2 * part] = mx[m] * c;
+        o.ml[2 * part + 1] = sum[m];
+      }
+      continue;
     }
+    const float inv = sum[m] == 0.0f ? 0.0f : 1.0f / sum[m];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+      store4<T>(static_cast<T*>(a.o) + orow[m] * D + 16 * d + 4 * g, acc[m][d][0] * inv,
+                acc[m][d][1] * inv, acc[m][d][2] * inv, acc[m][d][3] * inv);
   }
 }
 
 // Joins the splits of a query row: a wave per row, D/64 columns a lane.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(KvArgs a, int wave_rows, int splits) {
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(KvArgs a, int block_rows,
+                                                             int splits) {
   const int lane = threadIdx.x & 63;
   const size_t at = static_cast<size_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
   if (at >= static_cast<size_t>(a.B) * a.T * a.H_q) return;
@@ -435,9 +701,9 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvArgs a, int wave_
   const int n = tokens_of(a, b);
   if (t >= n) return;
   const int group = a.H_q / a.H_kv;
-  // The keys of the tile of rows that this row was computed in.
+  // The keys of the block of rows that this row was computed in.
   const int row = t * group + hq % group;
-  const int last = min((row / wave_rows + 1) * wave_rows, n * group) - 1;
+  const int last = min((row / block_rows + 1) * block_rows, n * group) - 1;
   const int steps = (key_limit(a, b, last / group) + kTile - 1) / kTile;
   const int per = split_steps(steps, splits);
   const int used = max(1, (steps + per - 1) / per);
@@ -461,24 +727,32 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvArgs a, int wave_
 
 // How a call is cut.
 struct Plan {
-  bool share;      // the waves of a workgroup share one tile of rows
-  int wave_rows;   // query rows of a wave
+  bool few;        // the waves of a workgroup share one tile of 16 rows
+  int waves;       // of a workgroup
+  int block_rows;  // query rows of a workgroup
   int row_blocks;  // workgroups over the rows of a (batch row, kv head)
   int splits;      // workgroups over the keys
 };
 
 Plan plan_of(const KvArgs& a, int io_bf16) {
   const long long rows = static_cast<long long>(a.T) * (a.H_q / a.H_kv);
+  const long long steps = (static_cast<long long>(a.max_pages) * a.page + kTile - 1) / kTile;
   Plan p;
-  p.share = rows <= 64;
-  p.wave_rows = p.share || !io_bf16 ? 16 : 32;
-  const int block_rows = p.share ? 16 : p.wave_rows * (kThreads / 64);
-  p.row_blocks = static_cast<int>((rows + block_rows - 1) / block_rows);
+  p.few = rows <= 64;
+  p.waves = 4;
+  p.block_rows = p.few ? 16 : io_bf16 ? kRowsBlock<2> : kRowsBlock<1>;
+  p.row_blocks = static_cast<int>((rows + p.block_rows - 1) / p.block_rows);
+  const long long base = static_cast<long long>(a.B) * a.H_kv * p.row_blocks;
+  // Short tables over few rows: eight waves and no splits, so that one launch
+  // does it all.
+  if (p.few && steps <= 16 && base <= 256) {
+    p.waves = 8;
+    p.splits = 1;
+    return p;
+  }
   // Enough workgroups for every CU to hold several, as far as the table's
   // keys allow.
-  const long long base = static_cast<long long>(a.B) * a.H_kv * p.row_blocks;
-  const long long steps = (static_cast<long long>(a.max_pages) * a.page + kTile - 1) / kTile;
-  const long long want = (1024 + base - 1) / base;
+  const long long want = ((p.few ? 1024 : 512) + base - 1) / base;
   const long long most = steps / kMinSteps;
   p.splits = static_cast<int>(min(want, most));
   if (p.splits > 64) p.splits = 64;
@@ -490,19 +764,21 @@ template <typename T, int D>
 hipError_t launch_d(const KvArgs& a, hipStream_t stream) {
   const Plan p = plan_of(a, sizeof(T) == 2);
   const dim3 grid(static_cast<unsigned>(a.B) * a.H_kv * p.row_blocks * p.splits);
-  if (p.share) {
-    hipLaunchKernelGGL((attn_kernel<T, D, 1, true>), grid, dim3(kThreads), 0, stream, a,
+  constexpr int MT = sizeof(T) == 2 ? 2 : 1;
+  if (!p.few)
+    hipLaunchKernelGGL((attn_rows_kernel<T, D, MT>), grid, dim3(kThreads), 0, stream, a,
                        p.row_blocks, p.splits);
-  } else {
-    constexpr int MT = sizeof(T) == 2 ? 2 : 1;
-    hipLaunchKernelGGL((attn_kernel<T, D, MT, false>), grid, dim3(kThreads), 0, stream, a,
-                       p.row_blocks, p.splits);
-  }
+  else if (p.waves == 8)
+    hipLaunchKernelGGL((attn_few_kernel<T, D, 8>), grid, dim3(512), 0, stream, a, p.row_blocks,
+                       p.splits);
+  else
+    hipLaunchKernelGGL((attn_few_kernel<T, D, 4>), grid, dim3(256), 0, stream, a, p.row_blocks,
+                       p.splits);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const size_t rows = static_cast<size_t>(a.B) * a.T * a.H_q;
   hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(static_cast<unsigned>((rows + 3) / 4)),
-                     dim3(kThreads), 0, stream, a, p.wave_rows, p.splits);
+                     dim3(kThreads), 0, stream, a, p.block_rows, p.splits);
   return hipGetLastError();
 }
 
