@@ -144,44 +144,6 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
   const int part = rest % splits;
   const int block = row_blocks - 1 - rest / splits;  // longest first
   const int group = a.H_q / a.H_kv;
-  const int n = tokens_of(a, b);
-  const int row0 = block * 16;
-  if (row0 >= n * group) return;
-  const int last = min(row0 + 16, n * group) - 1;
-  const Span span{key_limit(a, b, row0 / group), key_limit(a, b, last / group)};
-
-  const int steps = (span.hi + kTile - 1) / kTile;
-  const int per = split_steps(steps, splits);
-  const int s_end = min((part + 1) * per, steps);
-  int step = part * per + wave;
-  if (splits > 1 && part * per >= steps && part > 0) return;  // not read by the join
-
-  // This lane's query rows: one per tile, column r.
-  int lim[MT];
-  size_t orow[MT];
-  bf16x8_t q[MT][QP][KS];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = row0 + 16 * m + r;
-    const bool on = row <= last;
-    const int t = on ? row / group : 0;
-    lim[m] = on ? key_limit(a, b, t) : 0;
-    orow[m] = (static_cast<size_t>(b) * a.T + t) * a.H_q + head * group + (on ? row % group : 0);
-    const T* src = static_cast<const T*>(a.q) + orow[m] * D + g * (D / 4);
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      float x[8];
-      load_row<T, 8>(src + 8 * s, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        bf16 p[QP];
-        split<QP>(x[i], p);
-#pragma unroll
-        for (int c = 0; c < QP; ++c) q[m][c][s][i] = p[c];
-      }
-    }
-  }
-
   const int* table = a.block_table + static_cast<size_t>(b) * a.max_pages;
   const int page_shift = __builtin_ctz(a.page);
   // The page of a 16-key group of step s, or -1.
@@ -212,6 +174,55 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
       vr[d] = *reinterpret_cast<const uint4*>(p + static_cast<size_t>(16 * d) * a.page);
   };
 
+  // Without splits a wave's first step does not depend on the row's length: its
+  // pages are looked up and its loads issued while that is on its way (a step
+  // past the end is not used).
+  int step = wave;
+  int idk = -1, idv = -1;
+  if (splits == 1 && a.n_pages > 0) {
+    idk = page_of(step, ka);
+    idv = page_of(step, g);
+    load_k(step, idk);
+  }
+
+  const int n = tokens_of(a, b);
+  const int row0 = block * 16;
+  if (row0 >= n * group) return;
+  const int last = min(row0 + 16, n * group) - 1;
+  const Span span{key_limit(a, b, row0 / group), key_limit(a, b, last / group)};
+
+  const int steps = (span.hi + kTile - 1) / kTile;
+  const int per = split_steps(steps, splits);
+  const int s_end = min((part + 1) * per, steps);
+  if (splits > 1) step = part * per + wave;
+  if (splits > 1 && part * per >= steps && part > 0) return;  // not read by the join
+
+  // This lane's query rows: one per tile, column r.
+  int lim[MT];
+  size_t orow[MT];
+  bf16x8_t q[MT][QP][KS];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = row0 + 16 * m + r;
+    const bool on = row <= last;
+    const int t = on ? row / group : 0;
+    lim[m] = on ? key_limit(a, b, t) : 0;
+    orow[m] = (static_cast<size_t>(b) * a.T + t) * a.H_q + head * group + (on ? row % group : 0);
+    const T* src = static_cast<const T*>(a.q) + orow[m] * D + g * (D / 4);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      float x[8];
+      load_row<T, 8>(src + 8 * s, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        bf16 p[QP];
+        split<QP>(x[i], p);
+#pragma unroll
+        for (int c = 0; c < QP; ++c) q[m][c][s][i] = p[c];
+      }
+    }
+  }
+
   f32x4 acc[MT][DT];
   float mx[MT], sum[MT];
 #pragma unroll
@@ -222,8 +233,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
     for (int d = 0; d < DT; ++d) acc[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  int idk = -1, idv = -1;
-  if (step < s_end) {
+  if (splits > 1 && step < s_end) {
     idk = page_of(step, ka);
     idv = page_of(step, g);
     load_k(step, idk);
@@ -327,11 +337,10 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
 #pragma unroll
           for (int k = 0; k < PP; ++k) p[m][k][i] = c[k];
         }
+      if (has_nan) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        unsigned w0 = word(vr[d], 2 * u), w1 = word(vr[d], 2 * u + 1);
-        if (has_nan) {
-          const bf16x8_t bad = nan_codes(w0, w1);
+        for (int d = 0; d < DT; ++d) {
+          const bf16x8_t bad = nan_codes(word(vr[d], 2 * u), word(vr[d], 2 * u + 1));
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -340,9 +349,14 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
             for (int e = 0; e < 4; ++e)
               if (hit[e] > 0.0f) acc[m][d][e] = NAN;
           }
-          w0 = without_nan(w0);
-          w1 = without_nan(w1);
+          const unsigned c0 = without_nan(word(vr[d], 2 * u));
+          const unsigned c1 = without_nan(word(vr[d], 2 * u + 1));
+          vr[d] = u == 0 ? make_uint4(c0, c1, vr[d].z, vr[d].w) : make_uint4(vr[d].x, vr[d].y, c0, c1);
         }
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const unsigned w0 = word(vr[d], 2 * u), w1 = word(vr[d], 2 * u + 1);
         const bf16x8_t v = codes_to_bf16(w0, w1);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -427,6 +441,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
   constexpr int LW = D / 64;  // 16-byte loads of a thread, of keys and of values
   __shared__ __attribute__((aligned(16))) Tile<D> tiles[2];
   __shared__ __attribute__((aligned(16))) int groups_on[2][kThreads / 64];
+  __shared__ unsigned long long nan_s[2][D];  // tokens of a step with NaN in a value channel
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -543,13 +558,27 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
 #pragma unroll 1
   for (; step < s_end; ++step) {
     Tile<D>& tile = tiles[step & 1];
-    bool odd = false;  // NaN among the values of a step that some rows see in part
+    bool odd = false;
     const bool block_whole = (step + 1) * kTile <= all.lo;
 #pragma unroll
     for (int i = 0; i < LW; ++i) {
       *reinterpret_cast<bf16x8_t*>(&tile.k[kt][kc + 16 * i]) = codes_to_bf16(kr[i][0], kr[i][1], ksc);
       *reinterpret_cast<bf16x8_t*>(&tile.k[kt][kc + 16 * i + 8]) =
           codes_to_bf16(kr[i][2], kr[i][3], ksc);
+      if (!block_whole) {
+        // A step that some rows see in part: NaN must not reach the others
+        // through p = 0, so it is taken out and noted, a bit for each token.
+        unsigned at = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if ((vr[i][k] >> (8 * j) & 0x7fu) == 0x7fu) at |= 1u << (4 * k + j);
+          vr[i][k] = without_nan(vr[i][k]);
+        }
+        reinterpret_cast<uint16_t*>(&nan_s[step & 1][vd])[vt + i] = static_cast<uint16_t>(at);
+        odd |= at != 0;
+      }
       const bf16x8_t v0 = codes_to_bf16(vr[i][0], vr[i][1], vsc[i]);
       const bf16x8_t v1 = codes_to_bf16(vr[i][2], vr[i][3], vsc[i]);
       bf16* vp = &tile.v[vd][32 * ((vt + i) / 2) + 4 * ((vt + i) & 1)];
@@ -557,9 +586,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
       *reinterpret_cast<bf16x4_t*>(vp + 8) = bf16x4_t{v0[4], v0[5], v0[6], v0[7]};
       *reinterpret_cast<bf16x4_t*>(vp + 16) = bf16x4_t{v1[0], v1[1], v1[2], v1[3]};
       *reinterpret_cast<bf16x4_t*>(vp + 24) = bf16x4_t{v1[4], v1[5], v1[6], v1[7]};
-      if (!block_whole)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) odd |= without_nan(vr[i][k]) != vr[i][k];
     }
     // A wave loads 16 neighbouring keys, all of one page: whether there is one.
     if (lane == 0) groups_on[step & 1][wave] = kid_now >= 0;
@@ -637,32 +663,31 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        bf16x8_t v = *reinterpret_cast<const bf16x8_t*>(&tile.v[16 * d + r][32 * u + 8 * g]);
-        if (has_nan && !whole) {
-          // NaN of keys that only some rows see: out of the product, and into
-          // the rows that see it.
-          bf16x8_t bad;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const bool is = !(v[i] == v[i]);
-            bad[i] = static_cast<bf16>(is ? 1.0f : 0.0f);
-            if (is) v[i] = static_cast<bf16>(0.0f);
-          }
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                bad, p[m][u][0], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (hit[e] > 0.0f) acc[m][d][e] = NAN;
-          }
-        }
+        const bf16x8_t v =
+            *reinterpret_cast<const bf16x8_t*>(&tile.v[16 * d + r][32 * u + 8 * g]);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int k = 0; k < PP; ++k)
             acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[m][u][k], acc[m][d], 0, 0, 0);
       }
+    if (has_nan) {
+      // A row that sees a key with NaN in a channel gets NaN there.
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int seen = min(max(lim[m] - step * kTile, 0), kTile);
+        unsigned long long vis = seen == kTile ? ~0ull : (1ull << seen) - 1;
+        if (!on.x) vis &= ~0xffffull;
+        if (!on.y) vis &= ~(0xffffull << 16);
+        if (!on.z) vis &= ~(0xffffull << 32);
+        if (!on.w) vis &= ~(0xffffull << 48);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (nan_s[step & 1][16 * d + 4 * g + e] & vis) acc[m][d][e] = NAN;
+      }
+    }
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -708,16 +733,30 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvArgs a, int block
   const int per = split_steps(steps, splits);
   const int used = max(1, (steps + per - 1) / per);
 
+  // Lane s takes split s's maximum and sum (at most 64 splits); then every
+  // lane adds up its columns.
   const Partial p = partial_of(a, splits, at);
-  float top = -INFINITY;
-  for (int s = 0; s < used; ++s) top = fmaxf(top, p.ml[2 * s]);
-  const float ref = top == -INFINITY ? 0.0f : top;
-  float tot = 0.0f, out[D / 64] = {};
-  for (int s = 0; s < used; ++s) {
-    const float f = __builtin_amdgcn_exp2f(p.ml[2 * s] - ref);
-    tot += f * p.ml[2 * s + 1];
+  const float ms = lane < used ? p.ml[2 * lane] : -INFINITY;
+  const float ls = lane < used ? p.ml[2 * lane + 1] : 0.0f;
+  float top = ms;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) out[i] += f * p.acc[s * D + lane * (D / 64) + i];
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  const float f = lane < used ? __builtin_amdgcn_exp2f(ms - (top == -INFINITY ? 0.0f : top)) : 0.0f;
+  const float tot = wave_sum(f * ls);
+  constexpr int kAhead = 8;  // splits requested together
+  float out[D / 64] = {};
+  for (int s0 = 0; s0 < used; s0 += kAhead) {
+    float x[kAhead][D / 64];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      load_row<float, D / 64>(p.acc + min(s0 + i, used - 1) * D + lane * (D / 64), x[i]);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float w = __shfl(f, (s0 + i) & 63, 64);
+      if (s0 + i < used)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) out[c] += w * x[i][c];
+    }
   }
   const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
 #pragma unroll
@@ -750,9 +789,10 @@ Plan plan_of(const KvArgs& a, int io_bf16) {
     p.splits = 1;
     return p;
   }
-  // Enough workgroups for every CU to hold several, as far as the table's
-  // keys allow.
-  const long long want = ((p.few ? 1024 : 512) + base - 1) / base;
+  // As many workgroups as the GPU holds at a time (two on each of 256 CUs), as
+  // far as the table's keys allow: with twice as many, 64 rows of 4096 to 8192
+  // keys take 171 us instead of 162, 16 rows of 2000 to 4000 35 instead of 29.
+  const long long want = 512 / base;
   const long long most = steps / kMinSteps;
   p.splits = static_cast<int>(min(want, most));
   if (p.splits > 64) p.splits = 64;
