@@ -54,6 +54,7 @@ template <int MT>
 constexpr int kRowsBlock = 16 * MT * (kThreads / 64);
 constexpr int kTile = 64;  // keys per step
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kSlack = 8.0f;  // how far (log2) a reference may lag behind the maximum
 
 // Eight e4m3 codes as bf16, times a power of two (exact).
 __device__ __forceinline__ bf16x8_t codes_to_bf16(unsigned w0, unsigned w1, float scale = 1.0f) {
@@ -496,47 +497,34 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
     }
   }
 
-  // Staging: thread tid loads channels kc ... + 16 LW - 1 of the step's key kt,
-  // and LW groups of 16 tokens of value channel vd.
+  // Staging: a wave loads 16 neighbouring keys of each step, all of one page, and
+  // their values.  The page, its scales and the bases are scalar; lane offsets
+  // do not change: 16 KW bytes of key lane / 4, and 16 tokens of channels lane,
+  // lane + 64.
   const int* table = a.block_table + static_cast<size_t>(b) * a.max_pages;
   const int page_shift = __builtin_ctz(a.page);
-  auto page_of = [&](int key) {
-    const int at = key >> page_shift;
+  auto page_of = [&](int s) {
+    const int at = (s * kTile + 16 * wave) >> page_shift;
     const int id = at < a.max_pages ? table[at] : -1;
-    return id >= 0 && id < a.n_pages ? id : -1;
+    return __builtin_amdgcn_readfirstlane(id >= 0 && id < a.n_pages ? id : -1);
   };
-  const int kt = tid >> 2, kc = (tid & 3) * 16 * LW;
-  const int vd = tid * LW / 4, vt = tid * LW % 4;  // channel, first group of 16 tokens
-  int kid = -1, kid_now = -1, vid[LW];
-  auto find = [&](int s) {
-    kid = page_of(s * kTile + kt);
-#pragma unroll
-    for (int i = 0; i < LW; ++i) vid[i] = page_of(s * kTile + 16 * (vt + i));
-  };
+  const int kt = 16 * wave + lane / 4, kc = lane % 4 * 16 * LW;
+  const unsigned koff = lane / 4 * D + kc, voff = lane * a.page;
   u32x4 kr[LW], vr[LW];
-  float ksc, vsc[LW];
+  float ksc = 1.0f, vsc = 1.0f;
+  int id_now = -1, id_next = -1;
   auto request = [&](int s) {
-    kid_now = kid;
-    const size_t kh = static_cast<size_t>(max(kid, 0)) * a.H_kv + head;
-    const uint8_t* kp = a.k_cache + (kh * a.page + ((s * kTile + kt) & (a.page - 1))) * D + kc;
-    ksc = a.k_scale[kh];
+    id_now = id_next;
+    const size_t ph = static_cast<size_t>(max(id_now, 0)) * a.H_kv + head;
+    const int slot = (s * kTile + 16 * wave) & (a.page - 1);
+    const uint8_t* kp = a.k_cache + (ph * a.page + slot) * D;
+    const uint8_t* vp = a.v_cache + ph * D * a.page + slot;
+    ksc = a.k_scale[ph];
+    vsc = a.v_scale[ph];
 #pragma unroll
     for (int i = 0; i < LW; ++i) {
-      kr[i] = *reinterpret_cast<const u32x4*>(kp + 16 * i);
-      const int key = s * kTile + 16 * (vt + i);
-      const size_t vh = static_cast<size_t>(max(vid[i], 0)) * a.H_kv + head;
-      vr[i] = *reinterpret_cast<const u32x4*>(a.v_cache + (vh * D + vd) * a.page +
-                                              (key & (a.page - 1)));
-      // Codes behind the last key, or of no page, count as zeros.
-      const int keep = vid[i] >= 0 ? min(max(all.hi - key, 0), 16) : 0;
-      vsc[i] = keep > 0 ? a.v_scale[vh] : 1.0f;
-      if (keep < 16) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int bytes = min(max(keep - 4 * k, 0), 4);
-          if (bytes < 4) vr[i][k] &= (1u << (8 * bytes)) - 1;
-        }
-      }
+      kr[i] = *reinterpret_cast<const u32x4*>(kp + koff + 16 * i);
+      vr[i] = *reinterpret_cast<const u32x4*>(vp + 64 * i * a.page + voff);
     }
   };
 
@@ -551,52 +539,62 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
   }
 
   if (step < s_end) {
-    find(step);
+    id_next = page_of(step);
     request(step);
-    if (step + 1 < s_end) find(step + 1);
+    if (step + 1 < s_end) id_next = page_of(step + 1);
   }
 #pragma unroll 1
   for (; step < s_end; ++step) {
     Tile<D>& tile = tiles[step & 1];
-    bool odd = false;
     const bool block_whole = (step + 1) * kTile <= all.lo;
+    bool odd = false;
+    float vs = vsc;
+    if (!block_whole) {
+      // A step that some rows see in part.  Codes behind the last key, or of no
+      // page, count as zeros.  NaN must not reach the rows that do not see its
+      // key through p = 0: it is taken out and noted, a bit for each token.
+      const int keep =
+          id_now >= 0 ? min(max(all.hi - step * kTile - 16 * wave, 0), 16) : 0;
+      if (keep == 0) vs = 1.0f;
 #pragma unroll
-    for (int i = 0; i < LW; ++i) {
-      *reinterpret_cast<bf16x8_t*>(&tile.k[kt][kc + 16 * i]) = codes_to_bf16(kr[i][0], kr[i][1], ksc);
-      *reinterpret_cast<bf16x8_t*>(&tile.k[kt][kc + 16 * i + 8]) =
-          codes_to_bf16(kr[i][2], kr[i][3], ksc);
-      if (!block_whole) {
-        // A step that some rows see in part: NaN must not reach the others
-        // through p = 0, so it is taken out and noted, a bit for each token.
+      for (int i = 0; i < LW; ++i) {
         unsigned at = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+          const int bytes = min(max(keep - 4 * k, 0), 4);
+          if (bytes < 4) vr[i][k] &= (1u << (8 * bytes)) - 1;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if ((vr[i][k] >> (8 * j) & 0x7fu) == 0x7fu) at |= 1u << (4 * k + j);
           vr[i][k] = without_nan(vr[i][k]);
         }
-        reinterpret_cast<uint16_t*>(&nan_s[step & 1][vd])[vt + i] = static_cast<uint16_t>(at);
+        reinterpret_cast<uint16_t*>(&nan_s[step & 1][lane + 64 * i])[wave] =
+            static_cast<uint16_t>(at);
         odd |= at != 0;
       }
-      const bf16x8_t v0 = codes_to_bf16(vr[i][0], vr[i][1], vsc[i]);
-      const bf16x8_t v1 = codes_to_bf16(vr[i][2], vr[i][3], vsc[i]);
-      bf16* vp = &tile.v[vd][32 * ((vt + i) / 2) + 4 * ((vt + i) & 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < LW; ++i) {
+      *reinterpret_cast<bf16x8_t*>(&tile.k[kt][kc + 16 * i]) = codes_to_bf16(kr[i][0], kr[i][1], ksc);
+      *reinterpret_cast<bf16x8_t*>(&tile.k[kt][kc + 16 * i + 8]) =
+          codes_to_bf16(kr[i][2], kr[i][3], ksc);
+      const bf16x8_t v0 = codes_to_bf16(vr[i][0], vr[i][1], vs);
+      const bf16x8_t v1 = codes_to_bf16(vr[i][2], vr[i][3], vs);
+      bf16* vp = &tile.v[lane + 64 * i][32 * (wave / 2) + 4 * (wave & 1)];
       *reinterpret_cast<bf16x4_t*>(vp) = bf16x4_t{v0[0], v0[1], v0[2], v0[3]};
       *reinterpret_cast<bf16x4_t*>(vp + 8) = bf16x4_t{v0[4], v0[5], v0[6], v0[7]};
       *reinterpret_cast<bf16x4_t*>(vp + 16) = bf16x4_t{v1[0], v1[1], v1[2], v1[3]};
       *reinterpret_cast<bf16x4_t*>(vp + 24) = bf16x4_t{v1[4], v1[5], v1[6], v1[7]};
     }
-    // A wave loads 16 neighbouring keys, all of one page: whether there is one.
-    if (lane == 0) groups_on[step & 1][wave] = kid_now >= 0;
+    if (lane == 0) groups_on[step & 1][wave] = id_now >= 0;
     bool has_nan = false;
     if (block_whole)
       __syncthreads();
     else
-      has_nan = __syncthreads_or(odd);
+      has_nan = __builtin_amdgcn_readfirstlane(__syncthreads_or(odd));
     if (step + 1 < s_end) {
       request(step + 1);
-      if (step + 2 < s_end) find(step + 2);
+      if (step + 2 < s_end) id_next = page_of(step + 2);
     }
     if (step * kTile >= span.hi) continue;  // nothing here for this wave's rows
 
@@ -615,20 +613,23 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
             z[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[m][p][s], z[m][t], 0, 0, 0);
       }
     }
-    const int4 on = *reinterpret_cast<const int4*>(groups_on[step & 1]);
-    const bool whole = (step + 1) * kTile <= span.lo && (on.x & on.y & on.z & on.w);
+    // Scalar, so that whole steps branch past the masks.
+    int on[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) on[t] = __builtin_amdgcn_readfirstlane(groups_on[step & 1][t]);
+    const bool whole = (step + 1) * kTile <= span.lo && (on[0] & on[1] & on[2] & on[3]);
     if (!whole) {
+      asm volatile("" ::: "memory");
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const bool there = t == 0 ? on.x : t == 1 ? on.y : t == 2 ? on.z : on.w;
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (!(there && step * kTile + 16 * t + 4 * g + e < lim[m])) z[m][t][e] = -INFINITY;
-        }
+            if (!(on[t] && step * kTile + 16 * t + 4 * g + e < lim[m])) z[m][t][e] = -INFINITY;
     }
-    bf16x8_t p[MT][2][PP];
+    float now[MT];
+    bool far = false;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       float top = -INFINITY;
@@ -638,15 +639,27 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
         for (int e = 0; e < 4; ++e) top = fmaxf(top, z[m][t][e]);
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float now = fmaxf(mx[m], top);
-      const float ref = now == -INFINITY ? 0.0f : now * c;
-      if (__any(now > mx[m])) {
-        const float back = __builtin_amdgcn_exp2f(__builtin_fmaf(mx[m], c, -ref));
+      now[m] = fmaxf(mx[m], top);
+      far |= (now[m] - mx[m]) * c > kSlack;
+    }
+    // mx is the running maximum or up to 2^kSlack (of p) below it: moving it
+    // rescales everything, and with 32 rows a wave some row's maximum moves in
+    // most steps.
+    if (__any(far)) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const float back = __builtin_amdgcn_exp2f(
+            __builtin_fmaf(mx[m], c, now[m] == -INFINITY ? 0.0f : -now[m] * c));
         sum[m] *= back;
 #pragma unroll
         for (int d = 0; d < DT; ++d) acc[m][d] *= back;
-        mx[m] = now;
+        mx[m] = now[m];
       }
+    }
+    bf16x8_t p[MT][2][PP];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float ref = mx[m] == -INFINITY ? 0.0f : mx[m] * c;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -672,15 +685,16 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
             acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[m][u][k], acc[m][d], 0, 0, 0);
       }
     if (has_nan) {
-      // A row that sees a key with NaN in a channel gets NaN there.
+      // A row that sees a key with NaN in a channel gets NaN there.  (The empty
+      // statement keeps this a branch: as selects it would run in every step.)
+      asm volatile("" ::: "memory");
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int seen = min(max(lim[m] - step * kTile, 0), kTile);
         unsigned long long vis = seen == kTile ? ~0ull : (1ull << seen) - 1;
-        if (!on.x) vis &= ~0xffffull;
-        if (!on.y) vis &= ~(0xffffull << 16);
-        if (!on.z) vis &= ~(0xffffull << 32);
-        if (!on.w) vis &= ~(0xffffull << 48);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (!on[t]) vis &= ~(0xffffull << (16 * t));
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
