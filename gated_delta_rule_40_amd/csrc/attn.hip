@@ -112,6 +112,7 @@ __device__ __forceinline__ int tokens_of(const KvArgs& a, int b) {
 
 // Steps of a split: at least kMinSteps, so that short rows use few splits.
 constexpr int kMinSteps = 4;
+constexpr int kMaxSplits = 64;
 __device__ __forceinline__ int split_steps(int steps, int splits) {
   return max(kMinSteps, (steps + splits - 1) / splits);
 }
@@ -728,12 +729,18 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
   }
 }
 
-// Joins the splits of a query row: a wave per row, D/64 columns a lane.
-template <typename T, int D>
+// Joins the splits of a query row, LANES lanes a row.  The loads of a row hang
+// on each other (length, splits, maxima, sums).  Where the rows alone fill the
+// GPU, 16 lanes put four rows of a wave under way together: 32768 rows of two
+// splits 8.7 us, at one row a wave 18.4; few rows of many splits (32 of 64)
+// want a whole wave each, 4 us less.
+template <typename T, int D, int LANES>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvArgs a, int block_rows,
                                                              int splits) {
-  const int lane = threadIdx.x & 63;
-  const size_t at = static_cast<size_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
+  constexpr int COLS = D / LANES;
+  constexpr int kMost = kMaxSplits / LANES;  // splits whose maximum a lane holds
+  const int l = threadIdx.x % LANES;
+  const size_t at = static_cast<size_t>(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
   if (at >= static_cast<size_t>(a.B) * a.T * a.H_q) return;
   const int hq = at % a.H_q;
   const int t = at / a.H_q % a.T, b = at / a.H_q / a.T;
@@ -747,35 +754,46 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvArgs a, int block
   const int per = split_steps(steps, splits);
   const int used = max(1, (steps + per - 1) / per);
 
-  // Lane s takes split s's maximum and sum (at most 64 splits); then every
-  // lane adds up its columns.
   const Partial p = partial_of(a, splits, at);
-  const float ms = lane < used ? p.ml[2 * lane] : -INFINITY;
-  const float ls = lane < used ? p.ml[2 * lane + 1] : 0.0f;
-  float top = ms;
+  float f[kMost], tot = 0.0f, top = -INFINITY;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-  const float f = lane < used ? __builtin_amdgcn_exp2f(ms - (top == -INFINITY ? 0.0f : top)) : 0.0f;
-  const float tot = wave_sum(f * ls);
+  for (int k = 0; k < kMost; ++k) {
+    const int s = LANES * k + l;
+    f[k] = s < used ? p.ml[2 * s] : -INFINITY;
+    top = fmaxf(top, f[k]);
+  }
+#pragma unroll
+  for (int o = 1; o < LANES; o *= 2) top = fmaxf(top, __shfl_xor(top, o, 64));
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const int s = LANES * k + l;
+    f[k] = s < used ? __builtin_amdgcn_exp2f(f[k] - (top == -INFINITY ? 0.0f : top)) : 0.0f;
+    if (s < used) tot += f[k] * p.ml[2 * s + 1];
+  }
+  tot = LANES == 16 ? row16_sum(tot) : wave_sum(tot);
+
+  float out[COLS] = {};
   constexpr int kAhead = 8;  // splits requested together
-  float out[D / 64] = {};
-  for (int s0 = 0; s0 < used; s0 += kAhead) {
-    float x[kAhead][D / 64];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      load_row<float, D / 64>(p.acc + min(s0 + i, used - 1) * D + lane * (D / 64), x[i]);
+  for (int k = 0; k < kMost; ++k) {
+    for (int s0 = LANES * k; s0 < min(used, LANES * (k + 1)); s0 += kAhead) {
+      float x[kAhead][COLS];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const float w = __shfl(f, (s0 + i) & 63, 64);
-      if (s0 + i < used)
+      for (int i = 0; i < kAhead; ++i)
+        load_row<float, COLS>(p.acc + min(s0 + i, used - 1) * D + l * COLS, x[i]);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) out[c] += w * x[i][c];
+      for (int i = 0; i < kAhead; ++i) {
+        const float w = __shfl(f[k], (s0 + i) % LANES, LANES);  // 0 past the last split
+        if (s0 + i < used)
+#pragma unroll
+          for (int c = 0; c < COLS; ++c) out[c] += w * x[i][c];
+      }
     }
   }
   const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i)
-    static_cast<T*>(a.o)[at * D + lane * (D / 64) + i] = from_f32<T>(out[i] * inv);
+  for (int c = 0; c < COLS; ++c)
+    static_cast<T*>(a.o)[at * D + l * COLS + c] = from_f32<T>(out[c] * inv);
 }
 
 // How a call is cut.
@@ -809,7 +827,7 @@ Plan plan_of(const KvArgs& a, int io_bf16) {
   const long long want = 512 / base;
   const long long most = steps / kMinSteps;
   p.splits = static_cast<int>(min(want, most));
-  if (p.splits > 64) p.splits = 64;
+  if (p.splits > kMaxSplits) p.splits = kMaxSplits;
   if (p.splits < 1) p.splits = 1;
   return p;
 }
@@ -831,8 +849,12 @@ hipError_t launch_d(const KvArgs& a, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const size_t rows = static_cast<size_t>(a.B) * a.T * a.H_q;
-  hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(static_cast<unsigned>((rows + 3) / 4)),
-                     dim3(kThreads), 0, stream, a, p.block_rows, p.splits);
+  if (rows > 8192)  // 8 waves on every SIMD at one row each
+    hipLaunchKernelGGL((attn_join_kernel<T, D, 16>), dim3(static_cast<unsigned>((rows + 15) / 16)),
+                       dim3(kThreads), 0, stream, a, p.block_rows, p.splits);
+  else
+    hipLaunchKernelGGL((attn_join_kernel<T, D, 64>), dim3(static_cast<unsigned>((rows + 3) / 4)),
+                       dim3(kThreads), 0, stream, a, p.block_rows, p.splits);
   return hipGetLastError();
 }
 
