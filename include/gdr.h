@@ -1,5 +1,7 @@
 /*
  * gdr.h -- C ABI of the gated delta rule library for AMD Instinct MI355X (gfx950).
+ * The layers beside it (short convolution, state space scan, attention over an
+ * 8-bit cache) follow in the second half.
  *
  * The gated delta rule is the GatedDeltaNet linear-attention recurrence.  Per
  * batch row b and value head h it keeps a state S (dk x dv, fp32) and, for each
@@ -375,8 +377,8 @@ typedef struct gdr_kv_dims {
  *   pos          [B] int32
  *   lens         [B] int32 or NULL
  *   caches, scales   updated in place; must not overlap an input.  Pages that
- *                the call writes must belong to one row each (two rows that
- *                write one page race, and its contents are then undefined)
+ *                the call writes must be named once in the table (two writers
+ *                of one page race, and its contents are then undefined)
  */
 int gdr_kv_append(const gdr_kv_dims* dims, gdr_dtype io, const void* k, const void* v,
                   const int32_t* block_table, const int32_t* pos, const int32_t* lens,

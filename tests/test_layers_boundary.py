@@ -125,6 +125,7 @@ def kv(attn=False, B=2, T=3, Hq=8, Hkv=2, D=64, page=32, n_pages=40, per=9, io=1
     (dict(D=96), "UNSUPPORTED"), (dict(D=256), "UNSUPPORTED"), (dict(page=48), "UNSUPPORTED"),
     (dict(page=256), "UNSUPPORTED"), (dict(page=8), "UNSUPPORTED"),
     (dict(B=2 ** 22), "SHAPE"), (dict(per=2 ** 26 + 1), "SHAPE"),
+    (dict(per=2 ** 26 - 1), "SHAPE"),              # the last step's end past 32 bits
     (dict(k=None), "NULL"), (dict(table=None), "NULL"), (dict(pos=None), "NULL"),
     (dict(kc=None), "NULL"), (dict(vc=None), "NULL"), (dict(ks=None), "NULL"),
     (dict(vs=None), "NULL"),
