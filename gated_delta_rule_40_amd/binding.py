@@ -242,26 +242,32 @@ _F32, _I32 = torch.float32, torch.int32
 _IO = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16}
 
 
-def _ptr(t, name, shape, dtype, device):
-    """Device address of a dense tensor of exactly this shape, dtype and device."""
-    try:
-        if (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
-            return t.data_ptr()
-    except AttributeError:
-        raise TypeError(f"{name} must be a torch.Tensor") from None
+def _refuse(t, name, shape, dtype, device):
+    """Raises with what is wrong with a tensor of a call."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def _opt(t, name, shape, dtype, device):
-    return None if t is None else _ptr(t, name, shape, dtype, device)
+# _ptr(t, name, shape, dtype, device): the address of a dense tensor of exactly
+# this shape, dtype and device (native, through _refuse for all others); _opt:
+# the same, None for None.
+try:
+    from . import _marshal
+except ImportError:
+    def _ptr(*_):
+        raise RuntimeError("_marshal.so is missing: build it with "
+                           "`python -m gated_delta_rule_40_amd.build`")
+    _opt = _ptr
+else:
+    _marshal.on_refusal(_refuse)
+    _ptr, _opt = _marshal.ptr, _marshal.opt
 
 
 def _lead(t, name, dims):
@@ -284,16 +290,18 @@ def _sized(struct):
 
 _conv_dims, _ssm_dims, _kv_dims = _sized(gdr_conv_dims), _sized(gdr_ssm_dims), _sized(gdr_kv_dims)
 
-# The current stream's handle as an integer: torch's own accessor for it where
-# there is one (0.1 us), else through a Stream object (2 us).
+# The current stream's handle as an integer, and the current device: torch's own
+# accessors where there are any (0.1 us), else through a Stream object (2 us) and
+# torch.cuda (0.3 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _launch(name, dev, stream, *args):
     """Calls an entry point with the stream as its last argument, on `dev`."""
     fn = getattr(_lib or load_library(), name)
-    index, here = dev.index, torch.cuda.current_device()
+    index, here = dev.index, _device()
     if index == here:
         rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     else:

@@ -1,8 +1,10 @@
-"""Build libgdr.so (the HIP kernels and the C ABI) for gfx950 with hipcc.
+"""Build libgdr.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and
+the binding's CPython extension _marshal.so with the host compiler.
 
 ``python -m gated_delta_rule_40_amd.build`` or ``build_library()`` compiles
 every source under ``csrc/`` to an object in ``_build/`` (in parallel) and
-links them into ``gated_delta_rule_40_amd/libgdr.so``.  It always recompiles.
+links them into ``gated_delta_rule_40_amd/libgdr.so``; ``csrc/python/`` goes
+into ``gated_delta_rule_40_amd/_marshal.so``.  It always recompiles.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -18,6 +21,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 BUILD_DIR = ROOT / "_build"
 LIB_PATH = PKG / "libgdr.so"
+MARSHAL_PATH = PKG / "_marshal.so"
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -63,12 +67,31 @@ def _compile(src: Path, verbose: bool) -> Path:
     return obj
 
 
+def _build_marshal() -> None:
+    import torch
+
+    t = Path(torch.__file__).resolve().parent
+    tmp = MARSHAL_PATH.with_name(f"{MARSHAL_PATH.name}.tmp{os.getpid()}")
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", str(t / "include"),
+           "-isystem", str(t / "include" / "torch" / "csrc" / "api" / "include"),
+           "-isystem", sysconfig.get_paths()["include"], str(CSRC / "python" / "marshal.cpp"),
+           f"-L{t / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-o", str(tmp)]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("compiling _marshal.so failed:\n" + res.stdout + res.stderr)
+    os.replace(tmp, MARSHAL_PATH)
+
+
 def build_library(verbose: bool = False, jobs: int | None = None) -> Path:
     BUILD_DIR.mkdir(exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs), max(1, (os.cpu_count() or 2)), 16)
     with ThreadPoolExecutor(jobs) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        marshal.result()
     tmp = LIB_PATH.with_name(f"{LIB_PATH.name}.tmp{os.getpid()}")
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *map(str, objs), "-o", str(tmp)]
     res = subprocess.run(cmd, capture_output=True, text=True)

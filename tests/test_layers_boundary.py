@@ -173,3 +173,27 @@ def test_binding_refuses_host_tensors():
         gdr.gdr_kv_append(z(2, 2, 64), z(2, 2, 64), None, None, None, None, None, None)
     with pytest.raises(TypeError):
         gdr.gdr_conv_step(None, None, None, None, None)
+
+
+def test_binding_checks_every_property_of_a_tensor():
+    from gated_delta_rule_40_amd.binding import _opt, _ptr
+    t = torch.zeros(3, 4)
+    cpu, f32 = torch.device("cpu"), torch.float32
+    assert _ptr(t, "t", (3, 4), f32, cpu) == t.data_ptr()
+    assert _ptr(torch.nn.Parameter(t), "t", t.shape, f32, cpu) == t.data_ptr()
+    assert _opt(None, "t", (3, 4), f32, cpu) is None
+    assert _opt(t, "t", (3, 4), f32, cpu) == t.data_ptr()
+    for args, error, text in [
+            ((t, "t", (4, 3), f32, cpu), ValueError, "shape"),
+            ((t, "t", (12,), f32, cpu), ValueError, "shape"),
+            ((t, "t", (3, 2 ** 70), f32, cpu), ValueError, "shape"),
+            ((t, "t", (3, 4), torch.bfloat16, cpu), ValueError, "dtype"),
+            ((t, "t", (3, 4), f32, torch.device("cuda", 0)), ValueError, "is on cpu"),
+            ((t.t(), "t", (4, 3), f32, cpu), ValueError, "contiguous"),
+            ((t.to_sparse(), "t", (3, 4), f32, cpu), (ValueError, RuntimeError), None),
+            ((None, "t", (3, 4), f32, cpu), TypeError, "torch.Tensor"),
+            ((5, "t", (3, 4), f32, cpu), TypeError, "torch.Tensor")]:
+        with pytest.raises(error, match=text):
+            _ptr(*args)
+    with pytest.raises(TypeError):
+        _ptr(t)
