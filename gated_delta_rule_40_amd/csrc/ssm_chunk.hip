@@ -56,6 +56,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int L = 64;  // tokens per chunk
+// Segments whose starts the walk adds up itself: four rows of 2000 tokens (4
+// segments) 124.7 -> 117.9 us; with 8 segments (two of 1500) 67.3 -> 74.7.
+constexpr int kFewSegs = 4;
 
 // 16 bytes, or zeros.
 __device__ __forceinline__ u32x4 load16_if(bool in, const void* p) {
@@ -367,22 +370,52 @@ __global__ __launch_bounds__(64 * NW, 2) void ssm_chunk_kernel(SsmArgs a, int bl
   const size_t unit = static_cast<size_t>(b) * a.H + head;
   float* starts = static_cast<float*>(a.ws);
   float* decays = starts + static_cast<size_t>(a.B) * a.H * segs * N * a.P;
+  // Where the walk starts: from the state before the first token, or the
+  // segment's start; with few segments that is added up here from the states of
+  // the segments before it, which saves ssm_start_kernel's launch.
   const float* from = nullptr;
+  const float* before = starts + unit * segs * N * a.P;  // segment k's state at k + 1
+  int add = 0;
   if (!kStates) {
-    if (segs > 1) from = starts + (unit * segs + seg) * N * a.P;
-    else if (a.state_in) from = a.state_in + unit * N * a.P;
+    if (segs > kFewSegs) {
+      from = before + static_cast<size_t>(seg) * N * a.P;
+    } else {
+      if (a.state_in) from = a.state_in + unit * N * a.P;
+      add = seg;
+    }
   }
+  // Element (16 k + 4 g + e, pcol + 16 ct + r) of a state; rows past N (the
+  // padding) are never reached, as k stays below N / 16.
+  constexpr int NK = N / 16;
+  auto at = [&](int k, int e, int ct) {
+    return static_cast<size_t>(16 * k + 4 * g + e) * a.P + pcol + 16 * ct + r;
+  };
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-    for (int k = 0; k < NTL; ++k)
+    for (int k = 0; k < NTL; ++k) S[ct][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // The branches lie around whole loads of a state, not around its elements.
+  if (from && on) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = 16 * k + 4 * g + e;
-        S[ct][k][e] = from && on && row < N
-                          ? from[static_cast<size_t>(row) * a.P + pcol + 16 * ct + r]
-                          : 0.0f;
-      }
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int k = 0; k < NK; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[ct][k][e] = from[at(k, e, ct)];
+  }
+  if (on) {
+#pragma unroll 1
+    for (int s = 0; s < add; ++s) {
+      const float f = __builtin_amdgcn_exp2f(decays[unit * segs + s]);
+      const float* m = before + static_cast<size_t>(s + 1) * N * a.P;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[ct][k][e] = f * S[ct][k][e] + m[at(k, e, ct)];
+    }
+  }
 
   if constexpr (Sh::NP > N) {  // the columns that the loads never write stay zeros
     for (int i = tid; i < L * Sh::NP; i += Sh::NT) {
@@ -603,12 +636,9 @@ __global__ __launch_bounds__(64 * NW, 2) void ssm_chunk_kernel(SsmArgs a, int bl
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int k = 0; k < NTL; ++k)
+      for (int k = 0; k < NK; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = 16 * k + 4 * g + e;
-          if (row < N) to[static_cast<size_t>(row) * a.P + pcol + 16 * ct + r] = S[ct][k][e];
-        }
+        for (int e = 0; e < 4; ++e) to[at(k, e, ct)] = S[ct][k][e];
   }
 }
 
@@ -690,9 +720,11 @@ hipError_t launch_shape(const SsmArgs& a, const Cut& c, hipStream_t stream) {
     hipLaunchKernelGGL((ssm_chunk_kernel<T, N, HB, NW, CT, true>), dim3(units * (c.segs - 1)),
                        dim3(States::NT), sizeof(States), stream, a, c.blocks, c.segs,
                        c.seg_chunks);
-    const size_t quads = static_cast<size_t>(a.B) * a.H * a.N * a.P / 4;
-    hipLaunchKernelGGL(ssm_start_kernel, dim3(static_cast<unsigned>((quads + 255) / 256)),
-                       dim3(256), 0, stream, a, c.segs);
+    if (c.segs > kFewSegs) {
+      const size_t quads = static_cast<size_t>(a.B) * a.H * a.N * a.P / 4;
+      hipLaunchKernelGGL(ssm_start_kernel, dim3(static_cast<unsigned>((quads + 255) / 256)),
+                         dim3(256), 0, stream, a, c.segs);
+    }
   }
   hipLaunchKernelGGL((ssm_chunk_kernel<T, N, HB, NW, CT, false>), dim3(units * c.segs),
                      dim3(Full::NT), sizeof(Full), stream, a, c.blocks, c.segs, c.seg_chunks);
