@@ -311,14 +311,20 @@ def _launch(name, dev, stream, *args):
         raise GdrError(rc, name)
 
 
+def _taps(weight):
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a tensor [C,W]")
+    return weight.shape[1]
+
+
 def gdr_conv_step(x, weight, bias, state, y, *, silu=True, stream=None):
     """One token of the short causal convolution.  x [B,C] (float32 or bfloat16;
     its rows may lie apart, as in a slice of a wider row), weight [C,W] fp32,
     bias [C] fp32 or None, state [B,W-1,C] in x's dtype (oldest input first,
     updated in place), y [B,C]."""
     (B, C), io, dev = _lead(x, "x", 2)
-    W = weight.shape[-1]
-    row = C if B <= 1 and x.is_contiguous() else x.stride(0)
+    W = _taps(weight)
+    row = x.stride(0) if B > 1 else C
     if x.stride(1) != 1 and C > 1:
         raise ValueError("x's channels must be contiguous")
     _launch("gdr_conv_step", dev, stream, _conv_dims(B, 1, W, C, 0, 0), io, int(bool(silu)),
@@ -334,12 +340,12 @@ def gdr_conv_prefill(x, weight, bias, state_in, state_out, outs, *, silu=True, l
     state_in (or None) and state_out [B,W-1,C], outs one to three tensors
     [B,T,c] whose widths add up to C, lens [B] int32 or None."""
     (B, T, C), io, dev = _lead(x, "x", 3)
-    W = weight.shape[-1]
+    W = _taps(weight)
     if x.is_contiguous():
         row = C
     else:
-        row = x.stride(1)
-        if x.stride(2) != 1 or (B > 1 and x.stride(0) != T * row):
+        row = x.stride(1) if T > 1 else x.stride(0) if B > 1 else C
+        if (x.stride(2) != 1 and C > 1) or (T > 1 and B > 1 and x.stride(0) != T * row):
             raise ValueError("x must be rows of contiguous channels, evenly apart")
     if not 1 <= len(outs) <= 3:
         raise ValueError(f"one to three outputs, got {len(outs)}")
@@ -409,10 +415,15 @@ def gdr_ssm_prefill(x, b, c, dt, A_log, dt_bias, D, state_in, state_out, y, work
             _ptr(state_out, "state_out", st, _F32, dev), rows(y, "y", H, P), ws, ws_bytes)
 
 
-def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table, pos, lens, B, H_kv, D, dev):
-    """Pool sizes and addresses of the cache's tensors."""
+def _pool_heads(k_cache):
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a tensor [n_pages,H_kv,page,D]")
+    return k_cache.shape[1]
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table, pos, lens, B, H_kv, D, dev):
+    """Pool sizes and addresses of the cache's tensors."""
+    _pool_heads(k_cache)
     if k_cache.dtype not in _F8:
         raise ValueError(f"k_cache has dtype {k_cache.dtype}, expected float8_e4m3fn or uint8")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
@@ -454,7 +465,7 @@ def gdr_attn_cached(q, k_cache, v_cache, k_scale, v_scale, block_table, pos, o, 
     gdr_kv_append, with the new tokens already written; workspace a uint8
     tensor of at least gdr_attn_workspace_size() bytes (None if that is 0)."""
     (B, T, H_q, D), io, dev = _lead(q, "q", 4)
-    H_kv = k_cache.shape[1]
+    H_kv = _pool_heads(k_cache)
     sizes, (kc, vc, ks, vs, bt, ps, ln) = _cache_args(k_cache, v_cache, k_scale, v_scale,
                                                       block_table, pos, lens, B, H_kv, D, dev)
     ws, ws_bytes = _space(workspace, dev)

@@ -53,6 +53,7 @@ int check_conv_sizes(const gdr_conv_dims* d, gdr_dtype io, gdr_act act, int T, i
   if (d->B < 0 || T < 0 || d->c0 <= 0 || d->c1 < 0 || d->c2 < 0) return GDR_E_SHAPE;
   const long long C = static_cast<long long>(d->c0) + d->c1 + d->c2;
   if (C > INT32_MAX || x_stride < C || (d->c2 > 0 && d->c1 == 0)) return GDR_E_SHAPE;
+  if (T > INT32_MAX - 64) return GDR_E_SHAPE;  // the end of the last tile is 32-bit
   if (d->W < 2 || d->W > 4) return GDR_E_UNSUPPORTED;
   if (gdr::conv_max_grid(d->B, T, static_cast<int>(C)) > gdr::kMaxGrid) return GDR_E_SHAPE;
   // Byte extents stay within 62 bits.

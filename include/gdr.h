@@ -43,7 +43,10 @@
  *     chunk in {16, 32, 64}.  B = 0 (and T = 0 for prefill) is a valid no-op.
  *     GDR_E_SHAPE also reports sizes past the 32-bit limits of the launch:
  *     B * H_v * dv and, for prefill, B * H_v * ceil(T / chunk) at most
- *     2^31 - 1, and chunk * H_v * dv at most 2^32 - 1.
+ *     2^31 - 1, and chunk * H_v * dv at most 2^32 - 1.  The layers in the
+ *     second half state theirs in the same way: workgroups within 2^24,
+ *     positions and lengths within 2^31 - 129, 256 H P and 256 G N bytes (a
+ *     chunk of the scan) within 2^32.
  */
 #ifndef GDR_H_
 #define GDR_H_

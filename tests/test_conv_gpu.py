@@ -97,6 +97,13 @@ def test_slices_of_wider_rows(lo, C, width, io):
     gdr.gdr_conv_prefill(g[:, :, lo: lo + C], gw, gb, gs, gs, [out])
     assert ref.worst(out.cpu(), want, ref.conv_bound(want, mag, x.dtype, W)) <= 1
     assert torch.equal(gs.cpu().to(ref.F64), st)
+    # One token a row: the rows lie a whole sequence apart.
+    one, st1 = torch.empty((B, 1, C), dtype=x.dtype, device=DEV), up(s0)[0]
+    gdr.gdr_conv_prefill(g[:, :1, lo: lo + C], gw, gb, st1, st1, [one])
+    assert torch.equal(one, out[:, :1])
+    one, st1 = torch.empty((1, 1, C), dtype=x.dtype, device=DEV), up(s0[:1].contiguous())[0]
+    gdr.gdr_conv_prefill(g[:1, :1, lo: lo + C], gw, gb, st1, st1, [one])
+    assert torch.equal(one, out[:1, :1])
     with pytest.raises(ValueError):
         gdr.gdr_conv_prefill(g[:, :-1, lo: lo + C], gw, gb, gs, gs, [out[:, :-1].contiguous()])
     with pytest.raises(ValueError):

@@ -48,6 +48,7 @@ def test_conv_refusals(step, case, expect):
 
 @pytest.mark.parametrize("case,expect", [
     (dict(T=-1), "SHAPE"), (dict(T=2 ** 31 - 1, B=2 ** 31 - 1), "SHAPE"),
+    (dict(T=2 ** 31 - 8, B=1, c=(4, 0, 0)), "SHAPE"),               # the last tile's end
     (dict(y=(A[5], None, A[7])), "NULL"), (dict(y=(A[5], A[6], None)), "NULL"),
     (dict(y=(A[5], A[5], A[7])), "ALIAS"), (dict(y=(A[5], A[6], A[6] + 16)), "ALIAS"),
     (dict(s_out=A[3] + 16), "ALIAS"), (dict(y=(A[3], A[6], A[7])), "ALIAS"),
