@@ -164,7 +164,7 @@ __device__ __forceinline__ float softplus_hw(float z) {
   p = __builtin_fmaf(p, q, 1.0f / 5.0f);
   p = __builtin_fmaf(p, q, 1.0f / 3.0f);
   p = __builtin_fmaf(p * q, s, s);
-  return (z > 0.0f ? z : 0.0f * z) + 2.0f * p;  // NaN stays
+  return fmaxf(z, 0.0f) + 2.0f * p;  // NaN stays, through p
 }
 
 }  // namespace gdr

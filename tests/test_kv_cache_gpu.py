@@ -292,3 +292,27 @@ def test_nan_token_does_not_reach_earlier_queries(Hq, T, io):
     cols = [d for d in range(64) if d != 7]
     assert torch.equal(o[:, :, :half][..., cols], clean[:, :, :half][..., cols])
     assert torch.isnan(o[:, at:, :half, 7]).all() and torch.isnan(o[:, at:, half:]).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 70])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
+def test_score_scales(scale, T, io):
+    """Negative, zero (the mean of the values in sight) and large score scales."""
+    require_gpu()
+    announce(f"attention with scale {scale} T={T} io={io}")
+    c = Cache(14, 2, 14, 1, 64, 16)
+    q = torch.randn(2, T, 2, 64).to(io_dtype(io))
+    pos = [90, 131]
+    check(c, q, attend(c, q, pos, scale), pos, scale)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_long_table_in_many_splits(io):
+    """One request with room for many more keys than it has, and one that uses them."""
+    require_gpu()
+    announce(f"attention over a long table io={io}")
+    c = Cache(15, 2, 160, 1, 64, 64)
+    q = torch.randn(2, 1, 2, 64).to(io_dtype(io))
+    pos = [20, 10200]
+    check(c, q, attend(c, q, pos, 0.125), pos, 0.125)

@@ -220,3 +220,15 @@ def test_nan_token_does_not_reach_earlier_ones(T, io):
     assert torch.isnan(y[0, at:, 1, 5]).all() and torch.isnan(s[0, 1, :, 5]).all()
     cols = [p for p in range(64) if p != 5]
     assert torch.equal(y[..., cols], clean[..., cols])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 8, 200])
+def test_dt_of_minus_infinity_leaves_the_state(T, io):
+    """softplus(-inf) = 0: such a token neither decays nor writes, and y = S^T C + D x."""
+    require_gpu()
+    announce(f"ssm dt = -inf T={T} io={io}")
+    d, s0 = inputs(11, 2, T, 1, 2, 32, 32, io)
+    d["dt"][0, T // 2:] = -math.inf
+    d["dt"][1, ::3] = -math.inf
+    check(d, s0, prefill(d, s0, 1))
