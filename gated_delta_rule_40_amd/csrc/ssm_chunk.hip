@@ -59,6 +59,13 @@ constexpr int L = 64;  // tokens per chunk
 // Segments whose starts the walk adds up itself: four rows of 2000 tokens (4
 // segments) 124.7 -> 117.9 us; with 8 segments (two of 1500) 67.3 -> 74.7.
 constexpr int kFewSegs = 4;
+// Whether ssm_start_kernel adds the starts up, into the workspace.  It has to
+// where the state is updated in place, however few the segments: the walk's last
+// segment writes state_out, and nothing orders that behind the other segments'
+// reads of state_in in the same launch.
+__host__ __device__ inline bool starts_joined(const SsmArgs& a, int segs) {
+  return segs > kFewSegs || (segs > 1 && a.state_in == a.state_out);
+}
 
 // 16 bytes, or zeros.
 __device__ __forceinline__ u32x4 load16_if(bool in, const void* p) {
@@ -371,13 +378,14 @@ __global__ __launch_bounds__(64 * NW, 2) void ssm_chunk_kernel(SsmArgs a, int bl
   float* starts = static_cast<float*>(a.ws);
   float* decays = starts + static_cast<size_t>(a.B) * a.H * segs * N * a.P;
   // Where the walk starts: from the state before the first token, or the
-  // segment's start; with few segments that is added up here from the states of
-  // the segments before it, which saves ssm_start_kernel's launch.
+  // segment's start; with few segments and a state that is not updated in place
+  // that is added up here from the states of the segments before it, which saves
+  // ssm_start_kernel's launch.
   const float* from = nullptr;
   const float* before = starts + unit * segs * N * a.P;  // segment k's state at k + 1
   int add = 0;
   if (!kStates) {
-    if (segs > kFewSegs) {
+    if (starts_joined(a, segs)) {
       from = before + static_cast<size_t>(seg) * N * a.P;
     } else {
       if (a.state_in) from = a.state_in + unit * N * a.P;
@@ -720,7 +728,7 @@ hipError_t launch_shape(const SsmArgs& a, const Cut& c, hipStream_t stream) {
     hipLaunchKernelGGL((ssm_chunk_kernel<T, N, HB, NW, CT, true>), dim3(units * (c.segs - 1)),
                        dim3(States::NT), sizeof(States), stream, a, c.blocks, c.segs,
                        c.seg_chunks);
-    if (c.segs > kFewSegs) {
+    if (starts_joined(a, c.segs)) {
       const size_t quads = static_cast<size_t>(a.B) * a.H * a.N * a.P / 4;
       hipLaunchKernelGGL(ssm_start_kernel, dim3(static_cast<unsigned>((quads + 255) / 256)),
                          dim3(256), 0, stream, a, c.segs);

@@ -232,3 +232,39 @@ def test_dt_of_minus_infinity_leaves_the_state(T, io):
     d["dt"][0, T // 2:] = -math.inf
     d["dt"][1, ::3] = -math.inf
     check(d, s0, prefill(d, s0, 1))
+
+
+@pytest.mark.parametrize("B,G,H,N,P,T,lens,io", [
+    (1, 1, 128, 128, 64, 449, None, "f32"), (1, 1, 128, 128, 64, 449, [40], "f32"),
+    (1, 1, 128, 128, 64, 321, [200], "f32"), (2, 8, 64, 128, 64, 2048, [1000, 2048], "bf16")])
+def test_in_place_with_more_segments_than_fit_at_once(B, G, H, N, P, T, lens, io):
+    """Two to four segments a row, more workgroups than the GPU holds, rows that
+    end before their last segment: no segment may start from what another one
+    has already written.  All heads against the call out of place, some heads
+    against the 64-bit form."""
+    require_gpu()
+    announce(f"ssm in place B={B} G={G} H={H} N={N} P={P} T={T} lens={lens} io={io}")
+    d, s0 = inputs(12, B, T, G, H, N, P, io)
+    apart = prefill(d, s0, G, lens)
+    got = prefill(d, s0, G, lens, in_place=True)
+    # Both are off by ssm_units of the sum of magnitudes at most, in bf16 by the
+    # roundings of `check` besides.  The magnitudes: the scan of absolute values.
+    mag, M = prefill(dict(d, x=d["x"].abs().float(), b=d["b"].abs().float(), c=d["c"].abs().float(),
+                          D=d["D"].abs()), s0.abs(), G, lens)
+    unit = ref.ssm_units(T, N) * EPS
+    bound = 2 * unit * mag + (2.0 ** -6 * mag if io == "bf16" else 0) + 1e-30
+    for b, n in enumerate(ref.clip_lens(lens, B, T)):
+        assert ref.worst(got[0][b, :n], apart[0][b, :n].double(), bound[b, :n]) <= 1
+        assert (got[0][b, n:] == 7).all()
+    assert ref.worst(got[1], apart[1].double(), 2 * unit * M + 1e-30) <= 1
+    heads, g = list(range(0, H, 16)), H // G
+    for b, n in enumerate(ref.clip_lens(lens, B, T)):
+        n = min(n, 450)                      # the 64-bit form's share of a long row
+        part = dict(d, **{k: d[k][b: b + 1, :n, heads] for k in ("x", "dt")},
+                    **{k: d[k][b: b + 1, :n, [h // g for h in heads]] for k in ("b", "c")},
+                    **{k: d[k][heads] for k in ("A_log", "dt_bias", "D")})
+        want, m, S, Ms = ref.ssm(**part, state=s0[b: b + 1, heads])
+        bd = unit * m + (2.0 ** -8 * (want.abs() + m) if io == "bf16" else 0) + 1e-30
+        assert ref.worst(got[0][b: b + 1, :n, heads], want, bd) <= 1
+        if n == ref.clip_lens(lens, B, T)[b]:
+            assert ref.worst(got[1][b: b + 1, heads], S, unit * Ms + 1e-30) <= 1
