@@ -550,12 +550,18 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
     const bool block_whole = (step + 1) * kTile <= all.lo;
     bool odd = false;
     float vs = vsc;
+    if (id_now < 0) {
+      // No page: the loads took page 0, whose codes and scale may be anything,
+      // and p = 0 would not take NaN out of the product.
+      vs = 1.0f;
+#pragma unroll
+      for (int i = 0; i < LW; ++i) vr[i] = u32x4{0u, 0u, 0u, 0u};
+    }
     if (!block_whole) {
-      // A step that some rows see in part.  Codes behind the last key, or of no
-      // page, count as zeros.  NaN must not reach the rows that do not see its
-      // key through p = 0: it is taken out and noted, a bit for each token.
-      const int keep =
-          id_now >= 0 ? min(max(all.hi - step * kTile - 16 * wave, 0), 16) : 0;
+      // A step that some rows see in part.  Codes behind the last key count as
+      // zeros.  NaN must not reach the rows that do not see its key through
+      // p = 0: it is taken out and noted, a bit for each token.
+      const int keep = min(max(all.hi - step * kTile - 16 * wave, 0), 16);
       if (keep == 0) vs = 1.0f;
 #pragma unroll
       for (int i = 0; i < LW; ++i) {

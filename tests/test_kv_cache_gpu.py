@@ -316,3 +316,26 @@ def test_long_table_in_many_splits(io):
     q = torch.randn(2, 1, 2, 64).to(io_dtype(io))
     pos = [20, 10200]
     check(c, q, attend(c, q, pos, 0.125), pos, 0.125)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 32), (64, 128)])
+@pytest.mark.parametrize("T", [1, 20, 70])
+def test_pages_outside_the_pool_count_for_nothing(T, D, page, io):
+    """Holes in the table among keys that every query sees; the pool's first page,
+    which no row names, holds NaN codes and scales that are not finite."""
+    require_gpu()
+    announce(f"attention with holes in the table T={T} D={D} page={page} io={io}")
+    B, keys = 2, 512 + T
+    c = Cache(16, B, -(-keys // page), 2, D, page)
+    c.table[c.table == 0] = next(p for p in range(1, c.pages) if not (c.table == p).any())
+    c.table[0, 0], c.table[1, 192 // page], c.table[1, 320 // page] = -1, c.pages, 2 ** 31 - 1
+    q = torch.randn(B, T, 4, D, generator=torch.Generator().manual_seed(T)).to(io_dtype(io))
+    pos, scale = [512, 400], 1 / math.sqrt(D)
+    clean = attend(c, q, pos, scale)
+    check(c, q, clean, pos, scale)
+    for ks, vs in ((math.nan, math.nan), (math.inf, math.inf)):
+        dev = c.device()
+        dev[0].view(torch.uint8)[0], dev[1].view(torch.uint8)[0] = 0x7F, 0xFF
+        dev[2][0], dev[3][0] = ks, vs
+        assert torch.equal(attend(c, q, pos, scale, dev=dev), clean)
