@@ -19,6 +19,7 @@
 #include "gdr.h"
 #include "gdr_internal.h"
 #include "kv_device.hpp"
+#include "kv_slots.hpp"
 
 namespace gdr {
 namespace {
@@ -34,12 +35,9 @@ __device__ __forceinline__ unsigned rescale(unsigned w, float ratio) {
 }
 
 // What workgroup `wg` writes: the slots of one page, of one head's keys or values.
-struct Target {
+struct Target : KvSlots {
   int b, head, is_v;
-  int u, w;       // slots [u, w) take new tokens; none if u >= w
-  int had;        // slots [0, had) hold older tokens of the row
-  int id;         // the page's number, unchecked
-  int first;      // the new token of slot u
+  int id;  // the page's number, unchecked
 };
 __device__ __forceinline__ Target target_of(const KvArgs& a, unsigned wg, int touched) {
   Target t = {};
@@ -50,16 +48,11 @@ __device__ __forceinline__ Target target_of(const KvArgs& a, unsigned wg, int to
   const int j = wg % touched;
   t.b = wg / touched;
   const int n = a.lens ? min(max(a.lens[t.b], 0), a.T) : a.T;
-  const long long pos = a.pos[t.b];
-  const long long start = pos > 0 ? pos : 0;
-  const long long page_no = start / a.page + j;
+  const int pos = a.pos[t.b];
+  const long long page_no = static_cast<long long>(max(pos, 0) / a.page) + j;
   if (page_no >= a.max_pages) return t;
+  static_cast<KvSlots&>(t) = kv_slots(pos, n, page_no, a.page);
   t.id = a.block_table[static_cast<size_t>(t.b) * a.max_pages + page_no];
-  const long long base = page_no * a.page;
-  t.u = static_cast<int>(max(start, base) - base);
-  t.w = static_cast<int>(min(pos + n, base + a.page) - base);
-  t.had = pos > base ? t.u : 0;
-  t.first = static_cast<int>(base + t.u - pos);
   return t;
 }
 

@@ -134,6 +134,21 @@ def test_append_does_not_follow_bad_pages():
         same(a, b)
 
 
+@pytest.mark.parametrize("T", [2, 8, 9, 33])
+@pytest.mark.parametrize("lens", [None, 0])
+def test_append_far_in_front_of_the_sequence_writes_nothing(T, lens):
+    """Positions near -2^31 (a sentinel for an idle row) are not followed."""
+    require_gpu()
+    announce(f"append at positions near -2^31 T={T} lens={lens}")
+    c = Cache(17, 4, 4, 2, 64, 16)
+    k = torch.randn(4, T, 2, 64)
+    pos = [-2 ** 31, -2 ** 31 + 1, -2 ** 31 + T, -T]
+    want = c.host()
+    got = append(c, k, -k, pos, None if lens is None else [lens] * 4)
+    for a, b in zip(got, want):
+        same(a, b)
+
+
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------
