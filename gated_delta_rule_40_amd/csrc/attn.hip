@@ -340,13 +340,21 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
           for (int k = 0; k < PP; ++k) p[m][k][i] = c[k];
         }
       if (has_nan) {
+        // The keys in sight, whatever their p: it may be too small for its type.
+        bf16x8_t see[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            see[m][i] = static_cast<bf16>(
+                group_on && key0 + 4 * (2 * u + i / 4) + (i & 3) < lim[m] ? 1.0f : 0.0f);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           const bf16x8_t bad = nan_codes(word(vr[d], 2 * u), word(vr[d], 2 * u + 1));
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                bad, p[m][0], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+                bad, see[m], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (hit[e] > 0.0f) acc[m][d][e] = NAN;

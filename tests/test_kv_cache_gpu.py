@@ -354,3 +354,27 @@ def test_pages_outside_the_pool_count_for_nothing(T, D, page, io):
         dev[0].view(torch.uint8)[0], dev[1].view(torch.uint8)[0] = 0x7F, 0xFF
         dev[2][0], dev[3][0] = ks, vs
         assert torch.equal(attend(c, q, pos, scale, dev=dev), clean)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 3, 70])
+@pytest.mark.parametrize("at", [5, 69])
+def test_nan_value_of_a_key_that_hardly_counts(at, T, io):
+    """NaN times a probability is NaN however small that is: past fp32's range, and
+    so with a value scale of 2^-100."""
+    require_gpu()
+    announce(f"attention, NaN value of a far key at={at} T={T} io={io}")
+    c = Cache(18, 2, 10, 1, 64, 16)
+    q = torch.randn(2, T, 4, 64).to(io_dtype(io))
+    q[..., 0] = 30.0
+    pos = [69, 80]
+    for b, k in ((0, -96.0), (1, -10.0)):               # p about e^-288, and e^-30 2^-100
+        pg = int(c.table[b, at // 16])
+        c.ks[pg], c.kc[pg, 0] = 1.0, 0.0
+        c.kc[pg, 0, at % 16, 0] = k
+        c.vc[pg, 0, 11, at % 16] = math.nan
+        if b == 1:
+            c.vs[pg] = 2.0 ** -100
+    o = attend(c, q, pos, 0.1)
+    assert torch.isnan(o[..., 11]).all()
+    assert torch.isfinite(o[..., [d for d in range(64) if d != 11]]).all()
