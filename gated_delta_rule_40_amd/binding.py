@@ -51,6 +51,21 @@ class gdr_kv_dims(ctypes.Structure):
                 for n in ("B", "T", "H_q", "H_kv", "D", "page", "n_pages", "max_pages")]
 
 
+def _sized(struct):
+    """Dimension structs by their sizes: a serving loop repeats a few.  ctypes would
+    wrap a size past 32 bits without a word."""
+    @functools.lru_cache(maxsize=256)
+    def make(*sizes):
+        for (name, _), n in zip(struct._fields_, sizes):
+            if not -2 ** 31 <= n < 2 ** 31:
+                raise ValueError(f"{name} = {n} does not fit 32 bits")
+        return struct(*sizes)
+    return make
+
+
+_dims, _conv_dims, _ssm_dims, _kv_dims = map(
+    _sized, (gdr_dims, gdr_conv_dims, gdr_ssm_dims, gdr_kv_dims))
+
 _lib = None
 
 
@@ -154,7 +169,7 @@ def gdr_decode_step(qkv, gate_in, beta_logit, state, o, *, H_qk, H_v, dk, dv, ga
         _check(state, "state", B * H_v * dk * dv, f32, dev),
         _check(o, "o", B * H_v * dv, qkv.dtype, dev),
     )
-    dims = gdr_dims(B, 1, H_qk, H_v, dk, dv, 0)
+    dims = _dims(B, 1, H_qk, H_v, dk, dv, 0)
     rc = lib.gdr_decode_step(ctypes.byref(dims), io, int(gate), args[0], args[1], args[2],
                              args[3], args[4], args[5], args[6], float(scale), int(bool(l2norm_qk)),
                              _stream(dev, stream))
@@ -163,7 +178,7 @@ def gdr_decode_step(qkv, gate_in, beta_logit, state, o, *, H_qk, H_v, dk, dv, ga
 
 
 def gdr_prefill_workspace_size(B, T, H_qk, H_v, dk, dv, chunk, io_dtype, gate) -> int:
-    dims = gdr_dims(B, T, H_qk, H_v, dk, dv, chunk)
+    dims = _dims(B, T, H_qk, H_v, dk, dv, chunk)
     return int(load_library().gdr_prefill_workspace_size(ctypes.byref(dims), _io_code(io_dtype),
                                                          int(gate)))
 
@@ -208,7 +223,7 @@ def gdr_prefill_chunked(q, k, v, gate_in, beta_logit, state_in, state_out, o, wo
         ws_ptr, ws_bytes = None, 0
     args = _prefill_args(q, k, v, gate_in, beta_logit, state_in, state_out, o, H_qk, H_v, dk, dv,
                          gate, A_log, dt_bias)
-    dims = gdr_dims(q.shape[0], q.shape[1], H_qk, H_v, dk, dv, chunk)
+    dims = _dims(q.shape[0], q.shape[1], H_qk, H_v, dk, dv, chunk)
     rc = lib.gdr_prefill_chunked(ctypes.byref(dims), _io_code(q.dtype), int(gate), *args,
                                  float(scale), int(bool(l2norm_qk)), ws_ptr,
                                  ctypes.c_size_t(ws_bytes), _stream(dev, stream))
@@ -225,7 +240,7 @@ def gdr_prefill_chunked_noalloc(q, k, v, gate_in, beta_logit, state_in, state_ou
     lib = load_library()
     args = _prefill_args(q, k, v, gate_in, beta_logit, state_in, state_out, o, H_qk, H_v, dk, dv,
                          gate, A_log, dt_bias)
-    dims = gdr_dims(q.shape[0], q.shape[1], H_qk, H_v, dk, dv, chunk)
+    dims = _dims(q.shape[0], q.shape[1], H_qk, H_v, dk, dv, chunk)
     rc = lib.gdr_prefill_chunked_noalloc(ctypes.byref(dims), _io_code(q.dtype), int(gate), *args,
                                          float(scale), int(bool(l2norm_qk)),
                                          _stream(q.device, stream))
@@ -281,14 +296,6 @@ def _lead(t, name, dims):
         raise ValueError(f"{name} is on {device}, expected a GPU")
     io = _IO.get(t.dtype)
     return shape, _io_code(t.dtype) if io is None else io, device
-
-
-def _sized(struct):
-    """Dimension structs by their sizes: a serving loop repeats a few."""
-    return functools.lru_cache(maxsize=256)(struct)
-
-
-_conv_dims, _ssm_dims, _kv_dims = _sized(gdr_conv_dims), _sized(gdr_ssm_dims), _sized(gdr_kv_dims)
 
 # The current stream's handle as an integer, and the current device: torch's own
 # accessors where there are any (0.1 us), else through a Stream object (2 us) and

@@ -198,3 +198,15 @@ def test_binding_checks_every_property_of_a_tensor():
             _ptr(*args)
     with pytest.raises(TypeError):
         _ptr(t)
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32, 2 ** 32 + 70, -2 ** 31 - 1])
+def test_binding_refuses_sizes_past_32_bits(big):
+    """Passed on as they are they would wrap: 2^32 + 70 tokens would be 70."""
+    bf = torch.bfloat16
+    with pytest.raises(ValueError, match="T = .* does not fit 32 bits"):
+        gdr.gdr_ssm_workspace_size(1, big, 1, 8, 128, 64, bf)
+    with pytest.raises(ValueError, match="max_pages = .* does not fit 32 bits"):
+        gdr.gdr_attn_workspace_size(1, 1, 8, 2, 128, 16, big, bf)
+    with pytest.raises(ValueError, match="T = .* does not fit 32 bits"):
+        gdr.gdr_prefill_workspace_size(1, big, 1, 2, 64, 64, 32, bf, gdr.GDR_GATE_SCALAR)
