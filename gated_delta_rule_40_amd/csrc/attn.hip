@@ -481,6 +481,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
   // exp2(c z - c m): c >= 0, the sign of the score scale goes to q; c = 0 would
   // lose masked keys' -inf.
   const float c = fmaxf(__builtin_fabsf(a.scale) * kLog2e, 1e-30f);
+  const float sign = a.scale < 0.0f ? -1.0f : a.scale == a.scale ? 1.0f : a.scale;  // NaN stays
   int lim[MT];
   size_t orow[MT];
   bf16x8_t q[MT][QP][KS];
@@ -499,7 +500,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         bf16 p[QP];
-        split<QP>(a.scale < 0.0f ? -x[i] : x[i], p);
+        split<QP>(sign * x[i], p);
 #pragma unroll
         for (int k = 0; k < QP; ++k) q[m][k][s][i] = p[k];
       }

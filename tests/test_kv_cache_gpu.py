@@ -378,3 +378,17 @@ def test_nan_value_of_a_key_that_hardly_counts(at, T, io):
     o = attend(c, q, pos, 0.1)
     assert torch.isnan(o[..., 11]).all()
     assert torch.isfinite(o[..., [d for d in range(64) if d != 11]]).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 70])
+@pytest.mark.parametrize("scale", [math.nan, math.inf])
+def test_score_scale_that_is_not_finite(scale, T, io):
+    """Scores of NaN, or of infinities and NaN: no finite answer, in either kernel;
+    queries with nothing to attend to still give zeros."""
+    require_gpu()
+    announce(f"attention with scale {scale} T={T} io={io}")
+    c = Cache(19, 2, 14, 1, 64, 16)
+    q = torch.randn(2, T, 2, 64).to(io_dtype(io))
+    o = attend(c, q, [90, -T], scale)
+    assert torch.isnan(o[0]).all() and (o[1] == 0).all()
