@@ -150,6 +150,13 @@ __device__ __forceinline__ float silu_hw(float x) {
   return x * __builtin_amdgcn_rcpf(1.0f + exp_hw(-x));
 }
 
+// -exp(A_log), held to fp32's largest value: an infinite rate would give NaN with
+// a step size of 0, which leaves the state as it is.  NaN stays.
+__device__ __forceinline__ float decay_rate(float A_log) {
+  const float r = expf(A_log);
+  return r > 3.402823466e38f ? -3.402823466e38f : -r;
+}
+
 // softplus(z) = max(z, 0) + log1p(u) with u = e^-|z| in (0, 1], to a few units
 // in the last place: log1p(u) = 2 atanh(s), s = u / (2 + u) <= 1/3, by the odd
 // series of atanh (its first term left out, s^17 / 17, is below 2^-30 of s).

@@ -63,7 +63,7 @@ __global__ __launch_bounds__((StepShape<N, P>::NT)) void ssm_step_kernel(SsmArgs
   for (int m = 0; m < RPT; ++m) s[m] = kNt ? __builtin_nontemporal_load(&S[m * C4]) : S[m * C4];
 
   const float d = softplusf(dt + db);
-  const float decay = expf(-expf(al) * d);
+  const float decay = expf(decay_rate(al) * d);
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int m = 0; m < RPT; ++m) {
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(64) void ssm_walk_kernel(SsmArgs a) {
   for (int m = 0; m < RPT; ++m)
     s[m] = a.state_in ? *reinterpret_cast<const float4*>(a.state_in + at + m * a.P)
                       : make_float4(0.f, 0.f, 0.f, 0.f);
-  const float rate = n > 0 ? -expf(a.A_log[h]) : 0.0f;  // T = 0 comes without parameters
+  const float rate = n > 0 ? decay_rate(a.A_log[h]) : 0.0f;  // T = 0 comes without parameters
   const float db = n > 0 && a.dt_bias ? a.dt_bias[h] : 0.0f;
   const float dskip = n > 0 && a.D ? a.D[h] : 0.0f;
 

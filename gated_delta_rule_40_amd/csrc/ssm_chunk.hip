@@ -228,7 +228,7 @@ struct Shape {
   T x[L][LX];
   T c[kStates ? 1 : L][LC];
   T p[kStates ? 1 : HB][L][LP];
-  float rate[HB], db[HB];  // -exp(A_log), dt_bias
+  float rate[HB], db[HB];  // decay_rate(A_log), dt_bias
   __device__ __forceinline__ T* brow(int row) { return b[row] + ((row >> 3) & 1) * EV; }
 };
 
@@ -266,7 +266,11 @@ __device__ __forceinline__ double wave_prefix_sum(double x) {
 // token is not there).
 __device__ __forceinline__ void form_rows(Rows& o, int lane, bool there, float z, float rate) {
   const float d = there ? softplus_hw(z) : 0.0f;
-  const double gam = wave_prefix_sum(static_cast<double>(rate) * d * 1.4426950408889634);
+  // Past 2^-1024 a token's decay is 0 times whatever fp32 holds; ending it there
+  // keeps the sums finite, and exact to 2^-32 behind such a token.
+  double g2 = static_cast<double>(rate) * d * 1.4426950408889634;
+  g2 = g2 < -1024.0 ? -1024.0 : g2;  // NaN stays
+  const double gam = wave_prefix_sum(g2);
   const float hi = static_cast<float>(gam);
   o.gh[lane] = hi;
   o.gl[lane] = static_cast<float>(gam - static_cast<double>(hi));
@@ -435,7 +439,7 @@ __global__ __launch_bounds__(64 * NW, 2) void ssm_chunk_kernel(SsmArgs a, int bl
 
   for (int hb = tid; hb < HB; hb += Sh::NT) {
     const int h = grp * rh + min(hb0 + hb, rh - 1);
-    sm.rate[hb] = -expf(a.A_log[h]);
+    sm.rate[hb] = decay_rate(a.A_log[h]);
     sm.db[hb] = a.dt_bias ? a.dt_bias[h] : 0.0f;
   }
   __syncthreads();

@@ -300,6 +300,8 @@ typedef struct gdr_ssm_dims {
  *     S <- exp(-exp(A_log[h]) d) S + d B x^T
  *     y  = S^T C + D[h] x
  *
+ * (exp(A_log) past fp32's largest value counts as that value.)
+ *
  *   xbc      [B, H*P + 2*G*N] io dtype: x heads, then B groups, then C groups
  *   dt       [B,H] fp32
  *   A_log    [H] fp32

@@ -268,3 +268,39 @@ def test_in_place_with_more_segments_than_fit_at_once(B, G, H, N, P, T, lens, io
         assert ref.worst(got[0][b: b + 1, :n, heads], want, bd) <= 1
         if n == ref.clip_lens(lens, B, T)[b]:
             assert ref.worst(got[1][b: b + 1, heads], S, unit * Ms + 1e-30) <= 1
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 8, 100, 500])
+def test_rates_past_the_largest_float(T, io):
+    """exp(A_log) of 2^128 and more: a token forgets everything before it, one with
+    a step size of 0 nothing.  Steps, the walk, chunks and segments agree."""
+    require_gpu()
+    announce(f"ssm rates past fp32 T={T} io={io}")
+    d, s0 = inputs(14, 2, T, 1, 4, 32, 32, io)
+    d["A_log"] = torch.tensor([88.8, 100.0, 1e4, 60.0])   # in 64 bits the third is infinite, too
+    d["dt"][:, ::3] = -math.inf
+    d["dt"][1, T // 2] = 4.0
+    lens = [T, (T + 1) // 2]
+    # The form takes the rate as it is; 1e4 stands for any that is as good as infinite.
+    known = dict(d, A_log=d["A_log"].clamp(max=700.0))
+    check(known, s0, prefill(d, s0, 1, lens), lens)
+    g, S = up(d), s0.to(DEV)
+    y, ys = torch.empty((2, 4, 32), dtype=g["x"].dtype, device=DEV), []
+    for t in range(min(T, 8)):
+        xbc = torch.cat([g[k][:, t].flatten(1) for k in ("x", "b", "c")], 1).contiguous()
+        gdr.gdr_ssm_step(xbc, g["dt"][:, t].contiguous(), g["A_log"], g["dt_bias"], g["D"], S, y,
+                         G=1, H=4, N=32, P=32)
+        ys.append(y.cpu())
+    cut = {k: v[:, :len(ys)] if k in ("x", "b", "c", "dt") else v for k, v in known.items()}
+    check(cut, s0, (torch.stack(ys, 1), S.cpu()))
+
+
+def test_differences_behind_an_enormous_decay_stay_exact():
+    """A step size of 1e30 in a chunk: the tokens behind it decay as without it."""
+    require_gpu()
+    announce("ssm enormous step size inside a chunk")
+    d, s0 = inputs(15, 1, 200, 1, 2, 16, 32, "f32")
+    d["dt"][0, [5, 70, 130]] = 1e30
+    d["x"][0, [5, 70, 130]] = 0.0                          # ... that writes nothing
+    check(d, s0, prefill(d, s0, 1))
