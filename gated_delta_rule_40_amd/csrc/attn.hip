@@ -21,9 +21,10 @@
 //     Q).  All loads go from the pages straight to registers.
 // e4m3 values are exact in bf16.  The key scales join the score scale, the
 // value scales (powers of two) multiply p.  p itself is split into bf16
-// pieces: two for bf16 io (2^-17 of it is lost, far below the output's own
-// rounding; one in attn_rows_kernel, where the second product is half the work:
-// a second rounding of the output's size), three, like q, for fp32 io (2^-25).
+// pieces, two for bf16 io and three, like q, for fp32 io, so that its rounding
+// stays far below the output's own (one piece would be a second rounding of that
+// size: 1024 queries over up to 3500 keys 70.7 instead of 82.4 us, but off by
+// 1.82e-3 of the norm where the output's rounding alone is 1.65e-3).
 //
 // Two kernels.  With few query rows (attn_few_kernel, the order above) the
 // waves of a workgroup share the keys and join in LDS: bound by HBM, one byte a
@@ -94,6 +95,31 @@ __device__ __forceinline__ void split(float x, bf16 (&out)[PIECES]) {
     out[i] = static_cast<bf16>(x);
     x -= static_cast<float>(out[i]);
   }
+}
+
+// Eight p's as PIECES matrix operands.  All but the last piece are cut off rather
+// than rounded (the upper halves of two words are one byte permutation, the
+// remainder is exact either way); of two pieces 2^-15 of p is lost, of three 2^-22.
+template <int PIECES>
+__device__ __forceinline__ void split8(f32x4 a, f32x4 b, bf16x8_t (&out)[PIECES]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+  u32x4_t w[PIECES];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x = i < 2 ? a[2 * i] : b[2 * i - 4], y = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+#pragma unroll
+    for (int k = 0; k + 1 < PIECES; ++k) {
+      const unsigned ux = __builtin_bit_cast(unsigned, x), uy = __builtin_bit_cast(unsigned, y);
+      w[k][i] = __builtin_amdgcn_perm(uy, ux, 0x07060302u);
+      x -= __builtin_bit_cast(float, ux & 0xffff0000u);
+      y -= __builtin_bit_cast(float, uy & 0xffff0000u);
+    }
+    w[PIECES - 1][i] =
+        __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{x, y}), bf16x2_t));
+  }
+#pragma unroll
+  for (int k = 0; k < PIECES; ++k) out[k] = __builtin_bit_cast(bf16x8_t, w[k]);
 }
 
 // The keys that query rows row0 ... row0 + rows - 1 of batch row b attend to:
@@ -446,7 +472,7 @@ template <typename T, int D, int MT>
 __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int row_blocks,
                                                                 int splits) {
   constexpr int QP = sizeof(T) == 4 ? 3 : 1;
-  constexpr int PP = sizeof(T) == 4 ? 3 : 1;
+  constexpr int PP = sizeof(T) == 4 ? 3 : 2;
   constexpr int KS = D / 32, DT = D / 16;
   constexpr int LW = D / 64;  // 16-byte loads of a thread, of keys and of values
   __shared__ __attribute__((aligned(16))) Tile<D> tiles[2];
@@ -672,7 +698,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
         mx[m] = now[m];
       }
     }
-    bf16x8_t p[MT][2][PP];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const float ref = mx[m] == -INFINITY ? 0.0f : mx[m] * c;
@@ -682,14 +707,14 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
         for (int e = 0; e < 4; ++e) {
           const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(z[m][t][e], c, -ref));
           sum[m] += x;
-          bf16 piece[PP];
-          split<PP>(x, piece);
-#pragma unroll
-          for (int k = 0; k < PP; ++k) p[m][t / 2][k][4 * (t & 1) + e] = piece[k];
+          z[m][t][e] = x;
         }
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) {
+      bf16x8_t p[MT][PP];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) split8<PP>(z[m][2 * u], z[m][2 * u + 1], p[m]);
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         const bf16x8_t v =
@@ -698,8 +723,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_rows_kernel(KvArgs a, int ro
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int k = 0; k < PP; ++k)
-            acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[m][u][k], acc[m][d], 0, 0, 0);
+            acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[m][k], acc[m][d], 0, 0, 0);
       }
+    }
     if (has_nan) {
       // A row that sees a key with NaN in a channel gets NaN there.  (The empty
       // statement keeps this a branch: as selects it would run in every step.)

@@ -392,3 +392,30 @@ def test_score_scale_that_is_not_finite(scale, T, io):
     q = torch.randn(2, T, 2, 64).to(io_dtype(io))
     o = attend(c, q, [90, -T], scale)
     assert torch.isnan(o[0]).all() and (o[1] == 0).all()
+
+
+@pytest.mark.parametrize("T,Hq,D,page", [(1, 8, 64, 16), (40, 8, 128, 32), (150, 4, 64, 64),
+                                         (150, 8, 128, 16)])
+def test_bf16_outputs_round_once(T, Hq, D, page):
+    """bf16 outputs against the 64-bit form rounded once.  Scores are single exact
+    products, so what is off before the output's rounding is what p loses (2^-15 of
+    it), and fp32's units: the score's factor, product and difference at |z| log2(e)
+    <= 16 (48), exp2, p and the sums (32 + 4 sqrt(keys))."""
+    require_gpu()
+    announce(f"attention, one rounding T={T} Hq={Hq} D={D} page={page}")
+    gen = torch.Generator().manual_seed(T)
+    c = Cache(20, 1, -(-(300 + T) // page), 2, D, page)
+    c.ks[:], c.kc = 1.0, ref.e4m3(2 * torch.randn(c.kc.shape, generator=gen, dtype=torch.float64))
+    q = torch.zeros(1, T, Hq, D, dtype=torch.bfloat16)
+    q[0, :, :, torch.randperm(D, generator=gen)[0]] = 1.0
+    o = attend(c, q, [300], 1.0)
+    want, mag, top = ref.attention(q, c.kc, c.vc, c.ks, c.vs, c.table, [300], 1.0)
+    assert top.max() < 11
+    close = (2.0 ** -15 + (80 + 4 * (300 + T) ** 0.5) * 2.0 ** -24) * mag
+    assert ref.worst(o, want, 2.0 ** -8 * (want.abs() + close) + close + 1e-30) <= 1
+    # That leaves a difference only where a tie between two bf16 values lies within
+    # `close`: for 2 close / step of the values, a step each.  The step is 2^-7 of a
+    # value at most, so the mean square of the difference is at most
+    # 2 close 2^-7 |value|.
+    once = want.to(torch.bfloat16).double()
+    assert ((o.double() - once) ** 2).mean() <= (2.0 ** -6 * close * (want.abs() + close)).mean()
