@@ -19,15 +19,19 @@
 //      P_ij = G_ij e^(Gamma_i - Gamma_j) d_j to LDS;
 //   3. each wave, for its columns: y^T = e^Gamma S^T C^T + x^T P^T + D x^T
 //      and the state's update.
-// The state's accumulators are the S^T operand as they stand, with the rows of
-// C stored in the matching order; the transposed operands of B and x (bf16)
-// come through the transposing LDS loads.
+// Every product leaves its tiles as the next one's operands: the state's
+// accumulators are the S^T operand as they stand, with the rows of C stored in the
+// matching order, and a tile of P goes through LDS lane for lane; the transposed
+// operands of B and x (bf16) come through the transposing LDS loads, tokens in the
+// order of P's tiles.
 //
-// Roundings (bf16 io): P and the S^T operand round to bf16 once each before
-// their products, next to the output's own rounding of the same size.  The
-// state itself is an fp32 result: the weighted x is taken in three bf16 pieces
-// (2^-25 of it is lost), x and B are exact.  fp32 io runs on fp32 matrix
-// instructions throughout.
+// Roundings (bf16 io): P and the S^T operand are taken in two bf16 pieces (2^-15
+// of them is lost), so that the output's own rounding is the only one of its size;
+// in one piece each it would be off by 2.0e-3 instead of 1.7e-3 of the norm, up to
+// 19 roundings in single values, for 3% (4000 tokens 76.6 against 78.7 us) to 5%
+// (long rows 315 against 331) less time.  The state itself is an fp32 result: the
+// weighted x is taken in three bf16 pieces (2^-25 of it is lost), x and B are
+// exact.  fp32 io runs on fp32 matrix instructions throughout.
 //
 // Few units (rows x groups x column blocks) cannot fill the GPU by
 // themselves, so the chunks are then cut into segments: a first pass forms
@@ -35,10 +39,10 @@
 // ssm_start_kernel adds them up to every segment's start, and the second pass
 // walks the segments side by side.
 //
-// Bound by issue: per wave and chunk (two column tiles, N = 128) 955 vector, 150
-// matrix and 144 LDS instructions; a chunk takes 6.0 us on an idle GPU and 8.7 us
-// for two workgroups sharing a CU.  4000 tokens of 64 heads (N = 128, P = 64, 8
-// groups, bf16): segment states 23 us, their starts 9, the walk 47.
+// Bound by issue: per wave and chunk (two column tiles, N = 128) 1211 vector, 193
+// matrix and 150 LDS instructions, the waves waiting 39% of their cycles.  4000
+// tokens of 64 heads (N = 128, P = 64, 8 groups, bf16), by kernel: segment states
+// 23.5 us, their starts 10.6, the walk 48.1.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -74,13 +78,17 @@ __device__ __forceinline__ u32x4 load16_if(bool in, const void* p) {
   return v;
 }
 
-// Matrix operands of one io type, KS the width of a contraction step.  Lane l supplies row l % 16 with g = l / 16.
+// Matrix operands of one io type, KS the width of a contraction step.  Lane l
+// supplies row l % 16 with g = l / 16.  Contractions over the state's rows and over
+// tokens run in accumulator order: what a lane holds of a product is its operand of
+// the next.
 template <typename T>
 struct Op;
 
 template <>
 struct Op<bf16> {
   static constexpr int KS = 32, PIECES = 3;
+  static constexpr int HALVES = 2;  // of the state's and P's values
   using F = bf16x8_t;
   __device__ static __forceinline__ f32x4 mma(F a, F b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -88,16 +96,29 @@ struct Op<bf16> {
   __device__ static __forceinline__ F join(bf16x4_t a, bf16x4_t b) {
     return F{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   }
-  // Contraction over the state's rows in accumulator order: step s, lane group
-  // g takes rows 32 s + 4 g + {0..3} and 32 s + 16 + 4 g + {0..3}.
-  __device__ static __forceinline__ F state(const f32x4* acc, int s) {
-    F r;
+  // Two values as bf16 words: cut off, and what is left rounded (2^-15 is lost).
+  __device__ static __forceinline__ void halves(float x, float y, unsigned (&out)[HALVES]) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const unsigned ux = __builtin_bit_cast(unsigned, x), uy = __builtin_bit_cast(unsigned, y);
+    out[0] = __builtin_amdgcn_perm(uy, ux, 0x07060302u);
+    x -= __builtin_bit_cast(float, ux & 0xffff0000u);
+    y -= __builtin_bit_cast(float, uy & 0xffff0000u);
+    out[1] = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{x, y}), bf16x2_t));
+  }
+  // Step s, lane group g takes rows 32 s + 4 g + {0..3} and 32 s + 16 + 4 g + {0..3}.
+  __device__ static __forceinline__ void state(const f32x4* acc, int s, F (&out)[HALVES]) {
+    u32x4 w[HALVES];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      r[e] = static_cast<bf16>(acc[2 * s][e]);
-      r[4 + e] = static_cast<bf16>(acc[2 * s + 1][e]);
+    for (int i = 0; i < 4; ++i) {
+      const f32x4& t = acc[2 * s + i / 2];
+      unsigned h[HALVES];
+      halves(t[2 * (i & 1)], t[2 * (i & 1) + 1], h);
+#pragma unroll
+      for (int k = 0; k < HALVES; ++k) w[k][i] = h[k];
     }
-    return r;
+#pragma unroll
+    for (int k = 0; k < HALVES; ++k) out[k] = __builtin_bit_cast(F, w[k]);
   }
   __device__ static __forceinline__ F rows(const bf16* row, int s, int g) {
     return join(*reinterpret_cast<const bf16x4_t*>(row + 32 * s + 4 * g),
@@ -113,28 +134,24 @@ struct Op<bf16> {
     *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
     *reinterpret_cast<uint2*>(p + 8) = make_uint2(v.z, v.w);
   }
-  // Contraction over tokens, natural order: row operand and column operand.
-  __device__ static __forceinline__ F tokens(const bf16* row, int s, int g) {
-    return *reinterpret_cast<const F*>(row + 32 * s + 8 * g);
-  }
-  // Columns col0 + r of tokens 32 s + 8 g ... + 7: a transposing load takes 4
-  // tokens x 16 columns for each lane group, its lane r addressing token r / 4
-  // and columns 4 (r % 4), and hands lane r column r.
+  // Columns col0 + r of tokens 32 s + 4 g ... + 3 and 32 s + 16 + 4 g ... + 3: a
+  // transposing load takes 4 tokens x 16 columns for each lane group, its lane r
+  // addressing token r / 4 and columns 4 (r % 4), and hands lane r column r.
   // SHIFT: what every other eight rows lie further by.
   template <int SHIFT>
   __device__ static __forceinline__ F columns(const bf16* buf, int ld, int s, int g, int r,
                                               int col0) {
     typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-    const bf16* p = buf + (32 * s + 8 * g + r / 4) * ld + (g & 1) * SHIFT + col0 + 4 * (r & 3);
+    const bf16* p = buf + (32 * s + 4 * g + r / 4) * ld + (g >> 1) * SHIFT + col0 + 4 * (r & 3);
     const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
-    const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ld));
+    const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * ld));
     return join(__builtin_bit_cast(bf16x4_t, a), __builtin_bit_cast(bf16x4_t, b));
   }
   // x times per-token weights as pieces that add up to the product.
   __device__ static __forceinline__ void weigh(F x, const float* w, int s, int g,
                                                F (&out)[PIECES]) {
-    const float4 w0 = *reinterpret_cast<const float4*>(w + 32 * s + 8 * g);
-    const float4 w1 = *reinterpret_cast<const float4*>(w + 32 * s + 8 * g + 4);
+    const float4 w0 = *reinterpret_cast<const float4*>(w + 32 * s + 4 * g);
+    const float4 w1 = *reinterpret_cast<const float4*>(w + 32 * s + 16 + 4 * g);
     const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
@@ -162,13 +179,15 @@ struct Op<bf16> {
 
 template <>
 struct Op<float> {
-  static constexpr int KS = 4, PIECES = 1;
+  static constexpr int KS = 4, PIECES = 1, HALVES = 1;
   using F = float;
   __device__ static __forceinline__ f32x4 mma(F a, F b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
   }
   // Step s takes rows 16 (s / 4) + 4 g + s % 4.
-  __device__ static __forceinline__ F state(const f32x4* acc, int s) { return acc[s / 4][s & 3]; }
+  __device__ static __forceinline__ void state(const f32x4* acc, int s, F (&out)[HALVES]) {
+    out[0] = acc[s / 4][s & 3];
+  }
   __device__ static __forceinline__ F rows(const float* row, int s, int g) {
     return row[16 * (s / 4) + 4 * g + (s & 3)];
   }
@@ -178,17 +197,14 @@ struct Op<float> {
   __device__ static __forceinline__ void store_ordered(float* row, int c, u32x4 v) {
     *reinterpret_cast<u32x4*>(row + c) = v;
   }
-  __device__ static __forceinline__ F tokens(const float* row, int s, int g) {
-    return row[4 * s + g];
-  }
   template <int SHIFT>
   __device__ static __forceinline__ F columns(const float* buf, int ld, int s, int g, int r,
                                               int col0) {
-    return buf[(4 * s + g) * ld + ((s >> 1) & 1) * SHIFT + col0 + r];
+    return buf[(16 * (s / 4) + 4 * g + (s & 3)) * ld + (g >> 1) * SHIFT + col0 + r];
   }
   __device__ static __forceinline__ void weigh(F x, const float* w, int s, int g,
                                                F (&out)[PIECES]) {
-    out[0] = x * w[4 * s + g];
+    out[0] = x * w[16 * (s / 4) + 4 * g + (s & 3)];
   }
   __device__ static __forceinline__ float probe(F x, float sum) {
     return __builtin_fmaf(x, 0.0f, sum);
@@ -199,7 +215,6 @@ struct Op<float> {
 struct Rows {
   float gh[L], gl[L];  // Gamma as two floats
   float d[L];          // step size
-  float eg[L];         // e^Gamma
   float w[L];          // e^(Gamma_L - Gamma) d
   float rf[L];         // e^(Gamma - Gamma_m), m the last token before its 16
   float cf[96];        // e^(Gamma_m - Gamma) d of the tokens up to m, for m = 15, 31, 47
@@ -207,8 +222,79 @@ struct Rows {
   __device__ static __forceinline__ int at(int ti) { return 8 * ti * (ti - 1); }
 };
 
+// P of a head, as the operands that the products take: tile (ti, tj) of 16x16 is
+// written by one wave, lane for lane as it has it (rows i = r, columns 4 g + e), and
+// read by others in the same way.  Two tiles of a row that one contraction step
+// takes together lie side by side per lane.
+template <typename T>
+struct Tiles {
+  static constexpr int HALVES = Op<T>::HALVES;
+  T v[HALVES][10 * 256];
+  // The four values of a lane of tile (ti, tj); pairs begin at even tj.
+  __device__ static __forceinline__ int at(int ti, int tj, int lane) {
+    const int first = ti * (ti + 1) / 2 + (tj & ~1);
+    const bool pair = sizeof(T) == 2 && (tj | 1) <= ti;
+    return pair ? first * 256 + lane * 8 + (tj & 1) * 4
+                : (first + (tj & 1)) * 256 + lane * 4;
+  }
+  __device__ __forceinline__ void put(int ti, int tj, int lane, const float (&x)[4]) {
+    const int k = at(ti, tj, lane);
+    if constexpr (HALVES == 1) {
+      *reinterpret_cast<float4*>(&v[0][k]) = make_float4(x[0], x[1], x[2], x[3]);
+    } else {
+      unsigned a[HALVES], b[HALVES];
+      Op<T>::halves(x[0], x[1], a);
+      Op<T>::halves(x[2], x[3], b);
+#pragma unroll
+      for (int q = 0; q < HALVES; ++q)
+        *reinterpret_cast<uint2*>(&v[q][k]) = make_uint2(a[q], b[q]);
+    }
+  }
+  // The order in which the products of fp32 add up tokens.
+  __device__ static __forceinline__ int order(int k) {
+    return HALVES == 1 ? (k & ~15) + 4 * (k & 3) + (k >> 2 & 3) : k;
+  }
+  __device__ __forceinline__ float value(int k) const {
+    float x = to_f32(v[0][k]);
+#pragma unroll
+    for (int q = 1; q < HALVES; ++q) x += to_f32(v[q][k]);
+    return x;
+  }
+  // y^T += x^T P^T for tile row ti, x as columns of all tokens.
+  template <int CT, int KL>
+  __device__ __forceinline__ void multiply(int ti, int lane, const typename Op<T>::F (&x)[CT][KL],
+                                           f32x4 (&y)[CT]) const {
+    if constexpr (HALVES == 1) {
+#pragma unroll
+      for (int tj = 0; tj <= ti; ++tj) {
+        const f32x4 p = *reinterpret_cast<const f32x4*>(&v[0][at(ti, tj, lane)]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) y[ct] = Op<T>::mma(x[ct][4 * tj + e], p[e], y[ct]);
+      }
+    } else {
+#pragma unroll
+      for (int tj = 0; tj <= ti; tj += 2)
+#pragma unroll
+        for (int q = 0; q < HALVES; ++q) {
+          const T* from = &v[q][at(ti, tj, lane)];
+          bf16x8_t p;
+          if (tj < ti) {
+            p = *reinterpret_cast<const bf16x8_t*>(from);
+          } else {
+            const bf16x4_t h = *reinterpret_cast<const bf16x4_t*>(from);
+            p = Op<T>::join(h, bf16x4_t{});
+          }
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) y[ct] = Op<T>::mma(x[ct][tj / 2], p, y[ct]);
+        }
+    }
+  }
+};
+
 // A workgroup's LDS: NW waves of CT 16-column tiles, over HB heads.  The row
-// pitches keep the 16-byte reads of 16 rows (C, P) and the transposing reads
+// pitches keep the 16-byte reads of 16 rows (C) and the transposing reads
 // of 4 rows (B, x: 32 bytes a row, a pitch of 32 bytes more than a multiple of
 // 256) on distinct banks; B is also read 8 bytes from each of 16 rows, for
 // which every other eight rows lie 16 bytes further.
@@ -218,8 +304,7 @@ struct Shape {
   static constexpr int NP = N < Op<T>::KS ? Op<T>::KS : N;     // rows of the state, padded
   static constexpr int COLS = 16 * NW * CT;
   static constexpr int NT = 64 * NW;
-  static constexpr int LB = NP + 2 * EV, LC = NP + EV, LX = COLS + (COLS % 128 ? 1 : 2) * EV,
-                       LP = L + EV;
+  static constexpr int LB = NP + 2 * EV, LC = NP + EV, LX = COLS + (COLS % 128 ? 1 : 2) * EV;
   static constexpr int BV = (L * (N / EV) + NT - 1) / NT;  // 16-byte loads per thread
   static constexpr int XV = (L * (COLS / EV) + NT - 1) / NT;
   static_assert(HB <= NW, "a wave forms the rows of one head at a time");
@@ -227,7 +312,7 @@ struct Shape {
   T b[L][LB];
   T x[L][LX];
   T c[kStates ? 1 : L][LC];
-  T p[kStates ? 1 : HB][L][LP];
+  Tiles<T> p[kStates ? 1 : HB];
   float rate[HB], db[HB];  // decay_rate(A_log), dt_bias
   __device__ __forceinline__ T* brow(int row) { return b[row] + ((row >> 3) & 1) * EV; }
 };
@@ -275,7 +360,6 @@ __device__ __forceinline__ void form_rows(Rows& o, int lane, bool there, float z
   o.gh[lane] = hi;
   o.gl[lane] = static_cast<float>(gam - static_cast<double>(hi));
   o.d[lane] = d;
-  o.eg[lane] = __builtin_amdgcn_exp2f(hi);
   o.w[lane] = __builtin_amdgcn_exp2f(static_cast<float>(__shfl(gam, 63, 64) - gam)) * d;
   double before = 0.0;
 #pragma unroll
@@ -527,21 +611,39 @@ __global__ __launch_bounds__(64 * NW, 2) void ssm_chunk_kernel(SsmArgs a, int bl
               const float f = __builtin_amdgcn_exp2f((hi - jh[e]) + (lo - jl[e])) * jd[e];
               v[e] = j + e <= i ? acc[e] * f : 0.0f;
             }
-            // The tile right of the diagonal that a step of 32 tokens also takes.
-            if (O::KS > 16 && (ti & 1) == 0)
-              store4<T>(&sm.p[hb][i][j + 16], 0.f, 0.f, 0.f, 0.f);
           }
-          store4<T>(&sm.p[hb][i][j], v[0], v[1], v[2], v[3]);
+          sm.p[hb].put(ti, tj, lane, v);
         }
       }
       __syncthreads();
     }
 
     // ---- 3. this wave's columns ----
-    // Ahead of the other workgroup's staging and P (long rows 323 -> 314 us).
+    // Ahead of the other workgroup's staging and P (3% of long rows).
     __builtin_amdgcn_s_setprio(1);
     if (on) {
       const Rows& w = rows[hw];
+      f32x4 y[4][CT];  // of tile rows ti: first S^T C^T
+      if constexpr (!kStates) {
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) y[ti][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KN; ++s) {
+          F sf[CT][O::HALVES];
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) O::state(S[ct], s, sf[ct]);
+#pragma unroll
+          for (int ti = 0; ti < 4; ++ti) {
+            const F c = O::rows_ordered(sm.c[16 * ti + r], s, g);
+#pragma unroll
+            for (int q = 0; q < O::HALVES; ++q)
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct) y[ti][ct] = O::mma(sf[ct][q], c, y[ti][ct]);
+          }
+        }
+      }
       F xf[CT][KL];
       float sum = 0.0f;
 #pragma unroll
@@ -557,42 +659,26 @@ __global__ __launch_bounds__(64 * NW, 2) void ssm_chunk_kernel(SsmArgs a, int bl
         const bool plain = !__any(sum != 0.0f);
         char* yp = reinterpret_cast<char*>(static_cast<T*>(a.y) +
                                            (static_cast<size_t>(b) * a.T + t0) * xrow);
-        F sf[CT][KN];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-          for (int s = 0; s < KN; ++s) sf[ct][s] = O::state(S[ct], s);
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) {
           const int i = 16 * ti + r;
-          f32x4 y[CT];
+          const float eg = __builtin_amdgcn_exp2f(w.gh[i]);
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) y[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < KN; ++s) {
-            const F c = O::rows_ordered(sm.c[i], s, g);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) y[ct] = O::mma(sf[ct][s], c, y[ct]);
-          }
-          const float eg = w.eg[i];
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) y[ct] *= eg;
+          for (int ct = 0; ct < CT; ++ct) y[ti][ct] *= eg;
           if (plain) {
-#pragma unroll
-            for (int s = 0; s * O::KS < 16 * (ti + 1); ++s) {
-              const F p = O::tokens(sm.p[hw][i], s, g);
-#pragma unroll
-              for (int ct = 0; ct < CT; ++ct) y[ct] = O::mma(xf[ct][s], p, y[ct]);
-            }
+            sm.p[hw].multiply(ti, lane, xf, y[ti]);
           } else {
 #pragma unroll 1
-            for (int j = 0; j <= i; ++j) {
-              const float p = to_f32(sm.p[hw][i][j]);
+            for (int k = 0; k < 16 * (ti + 1); ++k) {
+              const int j = Tiles<T>::order(k);
+              if (j > i) continue;
+              const float p =
+                  sm.p[hw].value(Tiles<T>::at(ti, j / 16, r + 16 * (j / 4 % 4)) + j % 4);
 #pragma unroll
               for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  y[ct][e] += p * to_f32(sm.x[j][lcol + 16 * ct + 4 * g + e]);
+                  y[ti][ct][e] += p * to_f32(sm.x[j][lcol + 16 * ct + 4 * g + e]);
             }
           }
 #pragma unroll
@@ -601,12 +687,12 @@ __global__ __launch_bounds__(64 * NW, 2) void ssm_chunk_kernel(SsmArgs a, int bl
             load_row<T, 4>(&sm.x[i][lcol + 16 * ct + 4 * g], xv);
             if (t0 + i < n)
               store4<T>(reinterpret_cast<T*>(yp + 16 * ti * xrow * sizeof(T) + off_y) + 16 * ct,
-                        y[ct][0] + dskip * xv[0], y[ct][1] + dskip * xv[1],
-                        y[ct][2] + dskip * xv[2], y[ct][3] + dskip * xv[3]);
+                        y[ti][ct][0] + dskip * xv[0], y[ti][ct][1] + dskip * xv[1],
+                        y[ti][ct][2] + dskip * xv[2], y[ti][ct][3] + dskip * xv[3]);
           }
         }
       }
-      const float decay = w.eg[L - 1];
+      const float decay = __builtin_amdgcn_exp2f(w.gh[L - 1]);
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct)
 #pragma unroll

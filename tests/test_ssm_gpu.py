@@ -304,3 +304,25 @@ def test_differences_behind_an_enormous_decay_stay_exact():
     d["dt"][0, [5, 70, 130]] = 1e30
     d["x"][0, [5, 70, 130]] = 0.0                          # ... that writes nothing
     check(d, s0, prefill(d, s0, 1))
+
+
+@pytest.mark.parametrize("T,N,P,strong", [(100, 16, 32, True), (100, 128, 64, True),
+                                          (70, 16, 64, False), (130, 32, 128, True)])
+def test_bf16_outputs_round_once(T, N, P, strong):
+    """bf16 outputs of the chunks against the 64-bit form rounded once: a chunk's
+    weights and the state lose 2^-15 of themselves on their way into the products,
+    and a term is off by ssm_units of 2^-24 as in fp32."""
+    require_gpu()
+    announce(f"ssm, one rounding T={T} N={N} P={P} strong={strong}")
+    d, s0 = inputs(16, 2, T, 2, 4, N, P, "bf16", strong=strong)
+    d["D"] = None
+    y, _ = prefill(d, s0, 2)
+    want, mag, _, _ = ref.ssm(**d, state=s0)
+    close = (2.0 ** -15 + ref.ssm_units(T, N) * EPS) * mag
+    assert ref.worst(y, want, 2.0 ** -8 * (want.abs() + close) + close + 1e-30) <= 1
+    # That leaves a difference only where a tie between two bf16 values lies within
+    # `close`: for 2 close / step of the values, a step each.  The step is 2^-7 of a
+    # value at most, so the mean square of the difference is at most
+    # 2 close 2^-7 |value|.
+    once = want.to(torch.bfloat16).double()
+    assert ((y.double() - once) ** 2).mean() <= (2.0 ** -6 * close * (want.abs() + close)).mean()
