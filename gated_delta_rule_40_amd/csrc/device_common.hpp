@@ -140,9 +140,11 @@ __device__ __forceinline__ float fused_log_decay(float x, float A_log, float dt_
   return -expf(A_log) * softplusf(x + dt_bias);
 }
 
-// e^x and x sigmoid(x) through the hardware's exp2 and reciprocal (about one
-// unit in the last place each): where a value takes a handful of
-// multiply-adds, the library forms would cost more than all the rest.
+// e^x and x sigmoid(x) through the hardware's exp2 and reciprocal: where a value
+// takes a handful of multiply-adds, the library forms would cost more than all
+// the rest.  The product x log2(e) rounds before the exp2, which makes e^x off by
+// up to (1 + |x|) units in the last place, x sigmoid(x) by that for negative x
+// (where it is small) and by about three for others.
 __device__ __forceinline__ float exp_hw(float x) {
   return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
 }
@@ -157,11 +159,20 @@ __device__ __forceinline__ float decay_rate(float A_log) {
   return r > 3.402823466e38f ? -3.402823466e38f : -r;
 }
 
-// softplus(z) = max(z, 0) + log1p(u) with u = e^-|z| in (0, 1], to a few units
-// in the last place: log1p(u) = 2 atanh(s), s = u / (2 + u) <= 1/3, by the odd
-// series of atanh (its first term left out, s^17 / 17, is below 2^-30 of s).
+// softplus(z) = max(z, 0) + log1p(u) with u = e^-|z| in (0, 1], to a few units in
+// the last place (at most 2 seen from -70 to 85; log1pf(expf(z)) is off by 18 at
+// -70 and by 10 at -20): log1p(u) = 2 atanh(s), s = u / (2 + u) <= 1/3, by the odd
+// series of atanh (its first term left out, s^17 / 17, is below 2^-29.3 of s).  For
+// u, what rounding |z| log2(e) leaves out, and log2(e)'s own, is put back behind
+// the exp2.  u is 0 past |z| = 150, where the difference of infinities would be NaN.
 __device__ __forceinline__ float softplus_hw(float z) {
-  const float u = exp_hw(-__builtin_fabsf(z));
+  float x = __builtin_fabsf(z);
+  x = x > 150.0f ? 150.0f : x;  // NaN stays
+  constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925963033500e-8f;
+  const float t = x * -kHi;
+  const float left = __builtin_fmaf(x, -kLo, __builtin_fmaf(x, -kHi, -t));
+  float u = __builtin_amdgcn_exp2f(t);
+  u = __builtin_fmaf(u, left * 0.693147180559945f, u);
   const float s = u * __builtin_amdgcn_rcpf(2.0f + u), q = s * s;
   float p = 1.0f / 15.0f;
   p = __builtin_fmaf(p, q, 1.0f / 13.0f);

@@ -326,3 +326,34 @@ def test_bf16_outputs_round_once(T, N, P, strong):
     # 2 close 2^-7 |value|.
     once = want.to(torch.bfloat16).double()
     assert ((y.double() - once) ** 2).mean() <= (2.0 ** -6 * close * (want.abs() + close)).mean()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [8, 9, 100])
+def test_small_and_large_step_sizes(T, io):
+    """softplus from -85 to 85, one step size a head: the other tokens' are 0, so the
+    state is d B x, off by the softplus (8 units), the weight, its product with x and
+    that with B (4).  In steps and walks (up to 8 tokens) e^z comes from a product
+    with log2(e) that rounds before the exp2, as does the constant: 1.25 |z| units."""
+    require_gpu()
+    announce(f"ssm step sizes over the range T={T} io={io}")
+    zs = [-85.0, -70.3, -52.7, -33.1, -20.9, -9.77, -3.3, -0.51, 0.0, 0.3, 2.9, 7.7, 15.9, 31.0,
+          60.4, 85.0]
+    H = len(zs)
+    d, _ = inputs(17, 1, T, 1, H, 16, 16, io)
+    d["dt"][:] = -math.inf
+    d["dt"][0, T - 2] = torch.tensor(zs)
+    d["dt_bias"] = d["D"] = None
+    _, s = prefill(d, None, 1)
+    z = torch.tensor(zs).double()
+    step = torch.where(z > 30, z, torch.log1p(torch.exp(z.clamp(max=30))))
+    want = step[:, None, None] * d["b"][0, T - 2, 0].double()[None, :, None] \
+        * d["x"][0, T - 2].double()[:, None, :]
+    walk = 12 + 1.25 * z.abs()[:, None, None]
+    units = walk if T <= 8 else 12
+    assert ref.worst(s[0], want, units * EPS * want.abs() + 1e-37) <= 1
+    g, S = up(d), torch.zeros(1, H, 16, 16, device=DEV)
+    xbc = torch.cat([g[k][:, T - 2].flatten(1) for k in ("x", "b", "c")], 1).contiguous()
+    gdr.gdr_ssm_step(xbc, g["dt"][:, T - 2].contiguous(), g["A_log"], None, None, S,
+                     torch.empty((1, H, 16), dtype=xbc.dtype, device=DEV), G=1, H=H, N=16, P=16)
+    assert ref.worst(S[0].cpu(), want, walk * EPS * want.abs() + 1e-37) <= 1
