@@ -1,6 +1,8 @@
 """The short causal convolution on the GPU against its 64-bit form."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
@@ -141,3 +143,32 @@ def test_what_is_not_finite_stays_in_its_channel():
     assert torch.isnan(got[0, 4:8, 3]).all() and torch.isfinite(got[0, 8:, 3]).all()
     assert not torch.isfinite(got[0, 5:9, 9]).any() or w[9].min() < 0
     assert torch.isfinite(got[0, 9:, 9]).all()
+
+
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("io,C", [("f32", 16), ("f32", 15), ("bf16", 16), ("bf16", 13)])
+def test_infinite_inputs_follow_the_taps_sign(io, C, silu):
+    """An infinite input makes the W tokens of its window infinite with the sign of
+    its tap; the sigmoid takes minus infinity to NaN (0 times infinity).  C = 15 and
+    13 take one channel a thread."""
+    require_gpu()
+    announce(f"conv with infinities C={C} io={io} silu={silu}")
+    x, w, bias, s0 = inputs(3, 1, 12, C, 4, io)
+    w[:, 0], w[:, 1], w[:, 2], w[:, 3] = 0.5, -0.25, 1.5, -2.0
+    clean = x.clone()
+    x[0, 5, 9], x[0, 2, 4] = math.inf, -math.inf
+    want, mag, _ = ref.conv(clean, w, bias, s0, silu=silu)
+    bound = ref.conv_bound(want, mag, x.dtype, 4)
+    gw, gb, gs = up(w, bias, s0)
+    out = torch.empty((1, 12, C), dtype=x.dtype, device=DEV)
+    gdr.gdr_conv_prefill(x.to(DEV), gw, gb, gs, gs, [out], silu=silu)
+    got = out.cpu().double()
+    minus = math.nan if silu else -math.inf
+    touched = torch.zeros_like(want, dtype=torch.bool)
+    for t, c, plus in ((5, 9, 1), (2, 4, -1)):
+        for i in range(4):                                # tap 3 - i meets it i tokens later
+            rises = w[c, 3 - i] * plus > 0
+            v, e = got[0, t + i, c], math.inf if rises else minus
+            assert torch.isnan(v) if math.isnan(e) else v == e, (t + i, c)
+            touched[0, t + i, c] = True
+    assert ref.worst(got[~touched], want[~touched], bound[~touched]) <= 1
