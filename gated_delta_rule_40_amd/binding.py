@@ -275,10 +275,12 @@ def _refuse(t, name, shape, dtype, device):
 # the same, None for None.
 try:
     from . import _marshal
-except ImportError:
+except ImportError as _why:
+    _unloaded = _why  # missing, or built for another torch or Python
+
     def _ptr(*_):
-        raise RuntimeError("_marshal.so is missing: build it with "
-                           "`python -m gated_delta_rule_40_amd.build`")
+        raise RuntimeError(f"_marshal.so cannot be loaded ({_unloaded}): build it with "
+                           "`python -m gated_delta_rule_40_amd.build`") from _unloaded
     _opt = _ptr
 else:
     _marshal.on_refusal(_refuse)

@@ -4,10 +4,13 @@ the binding's CPython extension _marshal.so with the host compiler.
 ``python -m gated_delta_rule_40_amd.build`` or ``build_library()`` compiles
 every source under ``csrc/`` to an object in ``_build/`` (in parallel) and
 links them into ``gated_delta_rule_40_amd/libgdr.so``; ``csrc/python/`` goes
-into ``gated_delta_rule_40_amd/_marshal.so``.  It always recompiles.
+into ``gated_delta_rule_40_amd/_marshal.so``.  It always recompiles.  The C
+library needs hipcc alone; without torch or Python's headers the extension, which
+only the binding uses, is left out.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -67,7 +70,20 @@ def _compile(src: Path, verbose: bool) -> Path:
     return obj
 
 
+def _lacking() -> str | None:
+    """What the binding's extension would need and is not there."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if not (Path(sysconfig.get_paths()["include"]) / "Python.h").exists():
+        return "Python.h"
+    return None
+
+
 def _build_marshal() -> None:
+    lacking = _lacking()
+    if lacking:
+        print(f"{MARSHAL_PATH.name} is not built: no {lacking}", file=sys.stderr)
+        return
     import torch
 
     t = Path(torch.__file__).resolve().parent
@@ -91,13 +107,13 @@ def build_library(verbose: bool = False, jobs: int | None = None) -> Path:
     with ThreadPoolExecutor(jobs) as ex:
         marshal = ex.submit(_build_marshal)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        marshal.result()
     tmp = LIB_PATH.with_name(f"{LIB_PATH.name}.tmp{os.getpid()}")
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *map(str, objs), "-o", str(tmp)]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n" + res.stdout + res.stderr)
     os.replace(tmp, LIB_PATH)
+    marshal.result()  # raises if it failed, with the library in place
     return LIB_PATH
 
 
