@@ -169,7 +169,7 @@ const char* gdr_strerror(int status) {
     case GDR_E_WORKSPACE: return "workspace is NULL or smaller than the entry point's size query";
     case GDR_E_HIP: return "HIP runtime error at kernel launch";
     case GDR_E_ALIAS: return "an output, the state or the workspace overlaps a buffer it must not";
-    case GDR_E_ALIGN: return "tensor pointer is not 16-byte aligned";
+    case GDR_E_ALIGN: return "a tensor pointer is not aligned (16 bytes, for some tensors their element)";
     case GDR_E_SCRATCH:
       return "the call needs more workspace than the allocation-free entry point holds";
     default: return "unknown gdr status";

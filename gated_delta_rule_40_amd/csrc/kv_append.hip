@@ -13,8 +13,9 @@
 // (transposed values), rewriting older codes only if the scale grew.  Keys:
 // neighbouring threads along the channels, 16 D/8 bytes of a token together;
 // values: along the slots, so that a channel's row of the page goes out whole.
-// Bound by HBM (input read once, codes written once): 4 prompts of 1024 to
-// 2047 tokens, 8 heads of 128 in bf16, 38 MB.
+// Bound by latency, one round of loads and one of stores around the reduction: 4
+// prompts of 1024 to 2047 tokens, 8 heads of 128 in bf16, 38 MB, take 13 us (2.9
+// TB/s) where a copy of that size takes 7.
 #include "device_common.hpp"
 #include "gdr.h"
 #include "gdr_internal.h"

@@ -94,7 +94,8 @@ typedef enum gdr_status {
   GDR_E_HIP = -6,         /* the HIP runtime reported an error at launch        */
   GDR_E_ALIAS = -7,       /* o, the state or the workspace overlaps a buffer    */
                           /* it must not (see each entry point)                 */
-  GDR_E_ALIGN = -8,       /* a tensor is not 16-byte aligned                    */
+  GDR_E_ALIGN = -8,       /* a tensor is not 16-byte aligned (fp32 vectors and  */
+                          /* int32 tensors of the layers: to their element)     */
   GDR_E_SCRATCH = -9      /* the call needs more workspace than the             */
                           /* allocation-free entry point holds                  */
 } gdr_status;
@@ -229,6 +230,15 @@ int gdr_prefill_chunked_noalloc(const gdr_dims* dims, gdr_dtype io, gdr_gate gat
  * NULL for T tokens in every row), row b holds lens[b] tokens (taken as 0 if
  * negative, as T if larger).  Tokens behind them are not read, and their
  * output rows are left as they were.
+ *
+ * Alignment: tensors 16 bytes, but for fp32 vectors (bias, dt, A_log, dt_bias, D,
+ * scales) and int32 tensors (lens, pos, block_table), which need that of their
+ * element, and x of the convolution.
+ *
+ * Numbers: states, sums and softmax statistics are fp32 or wider.  An output in
+ * bf16 is rounded once, from a sum whose terms are within 2^-15 of themselves or
+ * better.  What depends on an input that is not finite may be infinite or NaN
+ * (which of the two can differ between a function's forms); nothing else is.
  * ------------------------------------------------------------------------ */
 
 /* Sizes of the short convolution: W taps over c0 + c1 + c2 channels, written
