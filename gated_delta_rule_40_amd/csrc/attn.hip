@@ -161,7 +161,6 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
   constexpr int KS = D / 32;                  // contraction steps of S^T
   constexpr int KW = D / 64;                  // 16-byte loads of a lane's key slice
   constexpr int DT = D / 16;                  // row tiles of O^T
-  constexpr int MT = 1;                       // tiles of query rows
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, g = lane >> 4;
 
@@ -225,41 +224,31 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
   if (splits > 1) step = part * per + wave;
   if (splits > 1 && part * per >= steps && part > 0) return;  // not read by the join
 
-  // This lane's query rows: one per tile, column r.
-  int lim[MT];
-  size_t orow[MT];
-  bf16x8_t q[MT][QP][KS];
+  // This lane's query row: column r.
+  bf16x8_t q[QP][KS];
+  const bool on = row0 + r <= last;
+  const int tok = on ? (row0 + r) / group : 0;
+  const int lim = on ? key_limit(a, b, tok) : 0;
+  const T* src = static_cast<const T*>(a.q) +
+                 ((static_cast<size_t>(b) * a.T + tok) * a.H_q + head * group +
+                  (on ? (row0 + r) % group : 0)) * D + g * (D / 4);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int row = row0 + 16 * m + r;
-    const bool on = row <= last;
-    const int t = on ? row / group : 0;
-    lim[m] = on ? key_limit(a, b, t) : 0;
-    orow[m] = (static_cast<size_t>(b) * a.T + t) * a.H_q + head * group + (on ? row % group : 0);
-    const T* src = static_cast<const T*>(a.q) + orow[m] * D + g * (D / 4);
+  for (int s = 0; s < KS; ++s) {
+    float x[8];
+    load_row<T, 8>(src + 8 * s, x);
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      float x[8];
-      load_row<T, 8>(src + 8 * s, x);
+    for (int i = 0; i < 8; ++i) {
+      bf16 p[QP];
+      split<QP>(x[i], p);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        bf16 p[QP];
-        split<QP>(x[i], p);
-#pragma unroll
-        for (int c = 0; c < QP; ++c) q[m][c][s][i] = p[c];
-      }
+      for (int c = 0; c < QP; ++c) q[c][s][i] = p[c];
     }
   }
 
-  f32x4 acc[MT][DT];
-  float mx[MT], sum[MT];
+  f32x4 acc[DT];
+  float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    mx[m] = -INFINITY;
-    sum[m] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) acc[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int d = 0; d < DT; ++d) acc[d] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   if (splits > 1 && step < s_end) {
     idk = page_of(step, ka);
@@ -278,20 +267,16 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
       idv2 = page_of(next, g);
     }
 
-    f32x4 z[MT][4];
+    f32x4 z[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) z[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const bf16x8_t k =
             codes_to_bf16(word(kr[t][s / 2], 2 * (s & 1)), word(kr[t][s / 2], 2 * (s & 1) + 1));
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int c = 0; c < QP; ++c)
-            z[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[m][c][s], z[m][t], 0, 0, 0);
+        for (int c = 0; c < QP; ++c)
+          z[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[c][s], z[t], 0, 0, 0);
       }
     }
     if (next < s_end) load_k(next, idk2);
@@ -301,38 +286,35 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
     const bool whole = (step + 1) * kTile <= span.lo && __all(idv >= 0);
     const bool group_on = idv >= 0 && key0 < span.hi;
     if (!whole && !group_on) vs = 0.0f;
+    float top = -INFINITY;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float top = -INFINITY;
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = z[m][t][e] * ks;
-          if (!whole && !(group_on && key0 + 4 * t + e < lim[m])) x = -INFINITY;
-          z[m][t][e] = x;
-          top = fmaxf(top, x);
-        }
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float now = fmaxf(mx[m], top);
-      if (__any(now > mx[m])) {
-        const float back = __builtin_amdgcn_exp2f(mx[m] - (now == -INFINITY ? 0.0f : now));
-        sum[m] *= back;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) acc[m][d] *= back;
-        mx[m] = now;
+      for (int e = 0; e < 4; ++e) {
+        float x = z[t][e] * ks;
+        if (!whole && !(group_on && key0 + 4 * t + e < lim)) x = -INFINITY;
+        z[t][e] = x;
+        top = fmaxf(top, x);
       }
-      const float ref = now == -INFINITY ? 0.0f : now;
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const float now = fmaxf(mx, top);
+    if (__any(now > mx)) {
+      const float back = __builtin_amdgcn_exp2f(mx - (now == -INFINITY ? 0.0f : now));
+      sum *= back;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = __builtin_amdgcn_exp2f(z[m][t][e] - ref);
-          sum[m] += p;
-          z[m][t][e] = p * vs;
-        }
+      for (int d = 0; d < DT; ++d) acc[d] *= back;
+      mx = now;
     }
+    const float ref = now == -INFINITY ? 0.0f : now;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p = __builtin_amdgcn_exp2f(z[t][e] - ref);
+        sum += p;
+        z[t][e] = p * vs;
+      }
 
     bool has_nan = false;
     if (!whole) {
@@ -355,36 +337,29 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
 
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      bf16x8_t p[MT][PP];
+      bf16x8_t p[PP];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int i = 0; i < 8; ++i) {
+        bf16 c[PP];
+        split<PP>(z[2 * u + i / 4][i & 3], c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          bf16 c[PP];
-          split<PP>(z[m][2 * u + i / 4][i & 3], c);
-#pragma unroll
-          for (int k = 0; k < PP; ++k) p[m][k][i] = c[k];
-        }
+        for (int k = 0; k < PP; ++k) p[k][i] = c[k];
+      }
       if (has_nan) {
         // The keys in sight, whatever their p: it may be too small for its type.
-        bf16x8_t see[MT];
+        bf16x8_t see;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            see[m][i] = static_cast<bf16>(
-                group_on && key0 + 4 * (2 * u + i / 4) + (i & 3) < lim[m] ? 1.0f : 0.0f);
+        for (int i = 0; i < 8; ++i)
+          see[i] = static_cast<bf16>(
+              group_on && key0 + 4 * (2 * u + i / 4) + (i & 3) < lim ? 1.0f : 0.0f);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           const bf16x8_t bad = nan_codes(word(vr[d], 2 * u), word(vr[d], 2 * u + 1));
+          const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              bad, see, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                bad, see[m], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (hit[e] > 0.0f) acc[m][d][e] = NAN;
-          }
+          for (int e = 0; e < 4; ++e)
+            if (hit[e] > 0.0f) acc[d][e] = NAN;
           const unsigned c0 = without_nan(word(vr[d], 2 * u));
           const unsigned c1 = without_nan(word(vr[d], 2 * u + 1));
           vr[d] = u == 0 ? make_uint4(c0, c1, vr[d].z, vr[d].w) : make_uint4(vr[d].x, vr[d].y, c0, c1);
@@ -395,31 +370,26 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
         const unsigned w0 = word(vr[d], 2 * u), w1 = word(vr[d], 2 * u + 1);
         const bf16x8_t v = codes_to_bf16(w0, w1);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int k = 0; k < PP; ++k)
-            acc[m][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[m][k], acc[m][d], 0, 0, 0);
+        for (int k = 0; k < PP; ++k)
+          acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[k], acc[d], 0, 0, 0);
       }
     }
     idk = idk2;
     idv = idv2;
   }
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    sum[m] += __shfl_xor(sum[m], 16, 64);
-    sum[m] += __shfl_xor(sum[m], 32, 64);
-  }
+  sum += __shfl_xor(sum, 16, 64);
+  sum += __shfl_xor(sum, 32, 64);
 
   // Join the waves' sums: every wave leaves its own in LDS, then 16 threads
   // share a row.
-    constexpr int LD = D + 4;
+  constexpr int LD = D + 4;
   __shared__ float acc_s[NW][16][LD], ml_s[NW][16][2];
 #pragma unroll
   for (int d = 0; d < DT; ++d)
-    *reinterpret_cast<f32x4*>(&acc_s[wave][r][16 * d + 4 * g]) = acc[0][d];
+    *reinterpret_cast<f32x4*>(&acc_s[wave][r][16 * d + 4 * g]) = acc[d];
   if (g == 0) {
-    ml_s[wave][r][0] = mx[0];
-    ml_s[wave][r][1] = sum[0];
+    ml_s[wave][r][0] = mx;
+    ml_s[wave][r][1] = sum;
   }
   __syncthreads();
   // Threads past the first 256 have no part in it.
@@ -850,6 +820,10 @@ Plan plan_of(const KvArgs& a, int io_bf16) {
   const long long rows = static_cast<long long>(a.T) * (a.H_q / a.H_kv);
   const long long steps = (static_cast<long long>(a.max_pages) * a.page + kTile - 1) / kTile;
   Plan p;
+  // Up to 64 rows go 16 to a workgroup, each reading all keys again; more share
+  // them.  Groups of 4 heads of 128, 64 rows against sharing: 16 requests of 2000 to
+  // 4000 keys 58 against 67 us, 64 of 1500 to 3000 163 against 153; 96 rows 85
+  // against 69 and 231 against 155 (one request 15.5 against 20.7).
   p.few = rows <= 64;
   p.waves = 4;
   p.block_rows = p.few ? 16 : io_bf16 ? kRowsBlock<2> : kRowsBlock<1>;
