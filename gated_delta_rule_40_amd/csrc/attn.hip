@@ -270,6 +270,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(KvArgs a, int row_blo
     f32x4 z[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
+      z[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const bf16x8_t k =

@@ -419,3 +419,18 @@ def test_bf16_outputs_round_once(T, Hq, D, page):
     # 2 close 2^-7 |value|.
     once = want.to(torch.bfloat16).double()
     assert ((o.double() - once) ** 2).mean() <= (2.0 ** -6 * close * (want.abs() + close)).mean()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,page,ctx", [
+    (29, 1, 5, 5, 128, 16, 1029), (10, 1, 12, 3, 64, 16, 2100), (3, 9, 2, 1, 64, 64, 1500)])
+def test_many_steps_a_wave(B, T, Hq, Hkv, D, page, ctx, io):
+    """Rows of many steps each, few and several query rows, large value scales: what
+    one step leaves in a wave's registers does not reach the next step's scores."""
+    require_gpu()
+    announce(f"attention of many steps B={B} T={T} Hq={Hq} Hkv={Hkv} D={D} page={page} io={io}")
+    c = Cache(21, B, -(-(ctx + T) // page), Hkv, D, page)
+    c.vs *= 2.0 ** 16
+    q = torch.randn(B, T, Hq, D, generator=torch.Generator().manual_seed(B)).to(io_dtype(io))
+    pos = [ctx - (53 * i) % (ctx // 2) for i in range(B)]
+    check(c, q, attend(c, q, pos, 1 / math.sqrt(D)), pos, 1 / math.sqrt(D))
