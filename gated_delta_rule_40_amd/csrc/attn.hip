@@ -98,8 +98,8 @@ __device__ __forceinline__ void split(float x, bf16 (&out)[PIECES]) {
 }
 
 // Eight p's as PIECES matrix operands.  All but the last piece are cut off rather
-// than rounded (the upper halves of two words are one byte permutation, the
-// remainder is exact either way); of two pieces 2^-15 of p is lost, of three 2^-22.
+// than rounded (the upper halves of two words are one byte permutation): three
+// pieces of eight bits hold a float whole, of two 2^-16 is lost.
 template <int PIECES>
 __device__ __forceinline__ void split8(f32x4 a, f32x4 b, bf16x8_t (&out)[PIECES]) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));

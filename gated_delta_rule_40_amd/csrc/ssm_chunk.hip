@@ -25,7 +25,7 @@
 // operands of B and x (bf16) come through the transposing LDS loads, tokens in the
 // order of P's tiles.
 //
-// Roundings (bf16 io): P and the S^T operand are taken in two bf16 pieces (2^-15
+// Roundings (bf16 io): P and the S^T operand are taken in two bf16 pieces (2^-16
 // of them is lost), so that the output's own rounding is the only one of its size;
 // in one piece each it would be off by 2.0e-3 instead of 1.7e-3 of the norm, up to
 // 19 roundings in single values, for 3% (4000 tokens 76.6 against 78.7 us) to 5%
@@ -60,8 +60,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int L = 64;  // tokens per chunk
-// Segments whose starts the walk adds up itself: four rows of 2000 tokens (4
-// segments) 124.7 -> 117.9 us; with 8 segments (two of 1500) 67.3 -> 74.7.
+// Segments whose starts the walk adds up itself, against a launch that does: four
+// rows of 2000 tokens (4 segments) 121 against 126 us, eight of 1000 (2 segments)
+// 114 against 124; with 8 segments (two of 1500) 74.7 against 67.3.
 constexpr int kFewSegs = 4;
 // Whether ssm_start_kernel adds the starts up, into the workspace.  It has to
 // where the state is updated in place, however few the segments: the walk's last
@@ -96,7 +97,7 @@ struct Op<bf16> {
   __device__ static __forceinline__ F join(bf16x4_t a, bf16x4_t b) {
     return F{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   }
-  // Two values as bf16 words: cut off, and what is left rounded (2^-15 is lost).
+  // Two values as bf16 words: cut off, and what is left rounded (2^-16 is lost).
   __device__ static __forceinline__ void halves(float x, float y, unsigned (&out)[HALVES]) {
     typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
     typedef float f32x2 __attribute__((ext_vector_type(2)));
