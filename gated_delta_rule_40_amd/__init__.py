@@ -20,6 +20,10 @@ and of the layers around it:
                                       gdr_ssm_workspace_size)
     gdr_kv_append, gdr_attn_cached    attention over a paged cache of e4m3 keys
                                       and values (gdr_attn_workspace_size)
+    gdr_rms_norm, gdr_quant_rows      norm of rows with a residual or a gate, rows of
+                                      e4m3 codes with a scale per 128 channels
+    gdr_matmul_fp8                    product of such rows with an e4m3 weight
+    gdr_rope, gdr_rope_freqs          rotary positions of packed q | k | v rows
 """
 from .binding import (  # noqa: F401
     GDR_BF16,
@@ -27,6 +31,11 @@ from .binding import (  # noqa: F401
     GDR_GATE_CHANNEL,
     GDR_GATE_SCALAR,
     GDR_GATE_SCALAR_FUSED,
+    GDR_ROPE_BASE,
+    GDR_ROPE_INDEX,
+    GDR_ROPE_LINEAR,
+    GDR_ROPE_NONE,
+    GDR_ROPE_TURNS,
     EXPORTED,
     GdrError,
     gdr_attn_cached,
@@ -35,9 +44,14 @@ from .binding import (  # noqa: F401
     gdr_conv_step,
     gdr_decode_step,
     gdr_kv_append,
+    gdr_matmul_fp8,
     gdr_prefill_chunked,
     gdr_prefill_chunked_noalloc,
     gdr_prefill_workspace_size,
+    gdr_quant_rows,
+    gdr_rms_norm,
+    gdr_rope,
+    gdr_rope_freqs,
     gdr_ssm_prefill,
     gdr_ssm_step,
     gdr_ssm_workspace_size,

@@ -18,13 +18,16 @@ import torch
 
 GDR_F32, GDR_BF16 = 0, 1
 GDR_GATE_CHANNEL, GDR_GATE_SCALAR, GDR_GATE_SCALAR_FUSED = 0, 1, 2
+GDR_NORM_GATE_NONE, GDR_NORM_GATE_AFTER, GDR_NORM_GATE_BEFORE = 0, 1, 2
+GDR_ROPE_NONE, GDR_ROPE_LINEAR, GDR_ROPE_BASE, GDR_ROPE_TURNS, GDR_ROPE_INDEX = 0, 1, 2, 3, 4
 GDR_OK = 0
 
 LIB_PATH = Path(__file__).resolve().parent / "libgdr.so"
 EXPORTED = ("gdr_decode_step", "gdr_prefill_workspace_size", "gdr_prefill_chunked",
             "gdr_prefill_chunked_noalloc", "gdr_conv_step", "gdr_conv_prefill", "gdr_ssm_step",
             "gdr_ssm_workspace_size", "gdr_ssm_prefill", "gdr_kv_append",
-            "gdr_attn_workspace_size", "gdr_attn_cached", "gdr_strerror")
+            "gdr_attn_workspace_size", "gdr_attn_cached", "gdr_rms_norm", "gdr_quant_rows",
+            "gdr_matmul_fp8", "gdr_rope", "gdr_rope_freqs", "gdr_strerror")
 NOALLOC_SCRATCH_BYTES = 128 << 20   # GDR_NOALLOC_SCRATCH_BYTES
 
 
@@ -51,6 +54,23 @@ class gdr_kv_dims(ctypes.Structure):
                 for n in ("B", "T", "H_q", "H_kv", "D", "page", "n_pages", "max_pages")]
 
 
+class gdr_norm_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("R", "H", "D")]
+
+
+class gdr_matmul_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K")]
+
+
+class gdr_rope_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "H_q", "H_kv", "D", "R")]
+
+
+class gdr_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32)] + [(n, ctypes.c_double)
+                                             for n in ("factor", "context", "low", "high")]
+
+
 def _sized(struct):
     """Dimension structs by their sizes: a serving loop repeats a few.  ctypes would
     wrap a size past 32 bits without a word."""
@@ -63,8 +83,9 @@ def _sized(struct):
     return make
 
 
-_dims, _conv_dims, _ssm_dims, _kv_dims = map(
-    _sized, (gdr_dims, gdr_conv_dims, gdr_ssm_dims, gdr_kv_dims))
+_dims, _conv_dims, _ssm_dims, _kv_dims, _norm_dims, _matmul_dims, _rope_dims = map(
+    _sized, (gdr_dims, gdr_conv_dims, gdr_ssm_dims, gdr_kv_dims, gdr_norm_dims, gdr_matmul_dims,
+             gdr_rope_dims))
 
 _lib = None
 
@@ -101,8 +122,17 @@ def load_library(path: Path | str | None = None):
     lib.gdr_kv_append.argtypes = [kv_p, i32] + [vp] * 10
     lib.gdr_attn_workspace_size.argtypes = [kv_p, i32]
     lib.gdr_attn_cached.argtypes = [kv_p, i32] + [vp] * 9 + [f32, vp, size, vp]
+    norm_p, mm_p, rope_p = (ctypes.POINTER(t)
+                            for t in (gdr_norm_dims, gdr_matmul_dims, gdr_rope_dims))
+    lib.gdr_rms_norm.argtypes = [norm_p, i32, vp, i64, i32, vp, i32, vp, i64, vp, f32] + [vp] * 4
+    lib.gdr_quant_rows.argtypes = [norm_p, i32, vp, i64, vp, vp, vp]
+    lib.gdr_matmul_fp8.argtypes = [mm_p, i32] + [vp] * 7
+    lib.gdr_rope.argtypes = [rope_p, i32, i32, vp, i64, vp, f32] + [vp] * 6
+    lib.gdr_rope_freqs.argtypes = [ctypes.c_int32, ctypes.c_double,
+                                   ctypes.POINTER(gdr_rope_scaling), vp, vp]
     for name in ("gdr_conv_step", "gdr_conv_prefill", "gdr_ssm_step", "gdr_ssm_prefill",
-                 "gdr_kv_append", "gdr_attn_cached"):
+                 "gdr_kv_append", "gdr_attn_cached", "gdr_rms_norm", "gdr_quant_rows",
+                 "gdr_matmul_fp8", "gdr_rope", "gdr_rope_freqs"):
         getattr(lib, name).restype = i32
     lib.gdr_ssm_workspace_size.restype = lib.gdr_attn_workspace_size.restype = size
     lib.gdr_strerror.argtypes = [i32]
@@ -481,3 +511,140 @@ def gdr_attn_cached(q, k_cache, v_cache, k_scale, v_scale, block_table, pos, o, 
     _launch("gdr_attn_cached", dev, stream, _kv_dims(B, T, H_q, H_kv, D, *sizes), io,
             _ptr(q, "q", (B, T, H_q, D), q.dtype, dev), kc, vc, ks, vs, bt, ps, ln,
             _ptr(o, "o", (B, T, H_q, D), q.dtype, dev), float(scale), ws, ws_bytes)
+
+
+def _rows(t, name):
+    """Sizes, dtype code, device and row stride of rows [R,W] whose channels are
+    contiguous (the rows may lie apart, as in a slice of a wider row)."""
+    (R, W), io, dev = _lead(t, name, 2)
+    if t.stride(1) != 1 and W > 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    return R, W, io, dev, t.stride(0) if R > 1 else W
+
+
+def _f8_rows(codes, scales, R, W, dev):
+    """Addresses of 8-bit rows and their scales (None for None)."""
+    if codes is None:
+        if scales is not None:
+            raise ValueError("scales without codes")
+        return None, None
+    if getattr(codes, "dtype", None) not in _F8:
+        raise ValueError("codes must be a float8_e4m3fn or uint8 tensor")
+    return (_ptr(codes, "codes", (R, W), codes.dtype, dev),
+            _ptr(scales, "scales", (R, -(-W // 128)), _F32, dev))
+
+
+def gdr_rms_norm(x, weight=None, y=None, codes=None, scales=None, *, residual=None, gate=None,
+                 gate_first=False, heads=None, eps=1e-6, stream=None):
+    """Root-mean-square norm of rows.  x [R,H*D] (float32 or bfloat16; its rows may
+    lie apart), weight [H,D] or [D] (H = 1) fp32; without one, `heads` is H (1 if
+    not given).  residual [R,H*D] (float32 or bfloat16; x is added to it in place
+    and the sum normed), gate [R,H*D] in x's dtype (rows may lie apart; its silu
+    multiplies the result, or x with gate_first).  Outputs: y [R,H*D] in x's dtype,
+    codes [R,H*D] (float8_e4m3fn or uint8) with scales [R,ceil(H*D/128)] fp32, or
+    both."""
+    R, W, io, dev, row = _rows(x, "x")
+    H = 1 if heads is None else heads
+    w = None
+    if weight is not None:
+        if not isinstance(weight, torch.Tensor) or weight.dim() not in (1, 2):
+            raise ValueError("weight must be a tensor [H,D] or [D]")
+        shape = weight.shape
+        H = shape[0] if len(shape) == 2 else 1
+        if heads is not None and heads != H:
+            raise ValueError(f"weight has {H} heads, expected {heads}")
+        w = _ptr(weight, "weight", (H, W // H) if len(shape) == 2 and H else (W,), _F32, dev)
+    if H < 1 or W % H:
+        raise ValueError(f"{W} channels are not {H} heads")
+    res, r = 0, None
+    if residual is not None:
+        res = _io_code(getattr(residual, "dtype", None))
+        r = _ptr(residual, "residual", (R, W), residual.dtype, dev)
+    order, g, g_row = GDR_NORM_GATE_NONE, None, 0
+    if gate is not None:
+        gr, gw, _, g_dev, g_row = _rows(gate, "gate")
+        if (gr, gw) != (R, W) or gate.dtype != x.dtype or g_dev != dev:
+            raise ValueError(f"gate must be like x: [{R},{W}], {x.dtype}, {dev}")
+        order, g = GDR_NORM_GATE_BEFORE if gate_first else GDR_NORM_GATE_AFTER, gate.data_ptr()
+    c, s = _f8_rows(codes, scales, R, W, dev)
+    _launch("gdr_rms_norm", dev, stream, _norm_dims(R, H, W // H), io, x.data_ptr(), row, res, r,
+            order, g, g_row, w, float(eps), _opt(y, "y", (R, W), x.dtype, dev), c, s)
+
+
+def gdr_quant_rows(x, codes, scales, *, stream=None):
+    """Rows x [R,K] (float32 or bfloat16; they may lie apart) to codes [R,K]
+    (float8_e4m3fn or uint8) and scales [R,ceil(K/128)] fp32."""
+    R, W, io, dev, row = _rows(x, "x")
+    if codes is None:
+        raise ValueError("codes is required")
+    c, s = _f8_rows(codes, scales, R, W, dev)
+    # Any width: rows of whole blocks are heads of 128 channels side by side.
+    H = W // 128 if W % 128 == 0 and W else 1
+    _launch("gdr_quant_rows", dev, stream, _norm_dims(R, H, W // H), io, x.data_ptr(), row, c, s)
+
+
+def gdr_matmul_fp8(x, x_scales, w, w_scales, y, *, bias=None, stream=None):
+    """Product of 8-bit rows x [M,K] (x_scales [M,ceil(K/128)] fp32) with an 8-bit
+    weight w [N,K] (w_scales [ceil(N/128),ceil(K/128)] fp32), codes float8_e4m3fn or
+    uint8: y [M,N] (float32 or bfloat16), bias [N] fp32 or None."""
+    (M, N), io, dev = _lead(y, "y", 2)
+    for name, t in (("x", x), ("w", w)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in _F8:
+            raise ValueError(f"{name} must be a float8_e4m3fn or uint8 tensor of two dimensions")
+    K = x.shape[1]
+    kb = -(-K // 128)
+    _launch("gdr_matmul_fp8", dev, stream, _matmul_dims(M, N, K), io,
+            _ptr(x, "x", (M, K), x.dtype, dev), _ptr(x_scales, "x_scales", (M, kb), _F32, dev),
+            _ptr(w, "w", (N, K), w.dtype, dev),
+            _ptr(w_scales, "w_scales", (-(-N // 128), kb), _F32, dev),
+            _opt(bias, "bias", (N,), _F32, dev), _ptr(y, "y", (M, N), y.dtype, dev))
+
+
+def gdr_rope(x, freq, pos, q, k, v=None, *, interleaved=False, magnitude=1.0, lens=None,
+             stream=None):
+    """Splits packed rows x [B,T,(H_q + 2 H_kv) D] (float32 or bfloat16; tokens may
+    lie apart, evenly over the whole batch) into q [B,T,H_q,D], k and v
+    [B,T,H_kv,D] and turns the first 2 len(freq) channels of q's and k's heads:
+    freq [R/2] float64 radians a position (gdr_rope_freqs), pos [B] int32 the
+    position of each row's first token, lens [B] int32 or None.  Without v the rows
+    hold q and k alone."""
+    (B, T, C), io, dev = _lead(x, "x", 3)
+    for name, t in (("q", q), ("k", k)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name} must be a tensor [B,T,heads,D]")
+    H_q, D = q.shape[2:]
+    H_kv = k.shape[2]
+    if C != (H_q + (1 if v is None else 2) * H_kv) * D:
+        raise ValueError(f"rows of {C} channels are not {H_q} + {H_kv} heads"
+                         f"{'' if v is None else f' + {H_kv}'} of {D}")
+    if x.is_contiguous():
+        row = C
+    else:
+        row = x.stride(1) if T > 1 else x.stride(0) if B > 1 else C
+        if (x.stride(2) != 1 and C > 1) or (T > 1 and B > 1 and x.stride(0) != T * row):
+            raise ValueError("x must be rows of contiguous channels, evenly apart")
+    if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
+        raise ValueError("freq must be a tensor [R/2]")
+    half = freq.shape[0]
+    _launch("gdr_rope", dev, stream, _rope_dims(B, T, H_q, H_kv, D, 2 * half), io,
+            int(bool(interleaved)), x.data_ptr(), row,
+            _ptr(freq, "freq", (half,), torch.float64, dev), float(magnitude),
+            _ptr(pos, "pos", (B,), _I32, dev), _opt(lens, "lens", (B,), _I32, dev),
+            _ptr(q, "q", (B, T, H_q, D), x.dtype, dev), _ptr(k, "k", (B, T, H_kv, D), x.dtype, dev),
+            _opt(v, "v", (B, T, H_kv, D), x.dtype, dev))
+
+
+def gdr_rope_freqs(R, base, *, kind=GDR_ROPE_NONE, factor=1.0, context=0.0, low=1.0, high=4.0):
+    """Frequencies [R/2] (a float64 tensor on the CPU) and the magnitude of gdr_rope
+    for heads of which R channels are turned; `kind` (GDR_ROPE_NONE, _LINEAR, _BASE,
+    _TURNS or _INDEX) says how they are stretched to `factor` times `context`."""
+    if not 2 <= R <= 512:
+        raise ValueError(f"R = {R}: expected an even number from 2 to 512")
+    freq = torch.empty(R // 2, dtype=torch.float64)
+    magnitude = ctypes.c_float()
+    s = gdr_rope_scaling(kind, factor, context, low, high)
+    rc = (_lib or load_library()).gdr_rope_freqs(R, base, ctypes.byref(s), freq.data_ptr(),
+                                                 ctypes.addressof(magnitude))
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_rope_freqs")
+    return freq, magnitude.value

@@ -4,8 +4,6 @@
 // synchronises; errors are returned before anything is enqueued.
 #include <stdint.h>
 
-#include <initializer_list>
-
 #include <hip/hip_runtime_api.h>
 
 #include "api_check.hpp"
@@ -15,35 +13,6 @@
 namespace {
 
 using namespace gdr::check;
-
-bool known_io(gdr_dtype io) { return io == GDR_F32 || io == GDR_BF16; }
-size_t size_of(gdr_dtype io) { return io == GDR_BF16 ? 2 : 4; }
-bool supported_width(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-
-int result(hipError_t e) { return e == hipSuccess ? GDR_OK : GDR_E_HIP; }
-
-// Whether a product of non-negative factors stays within `limit`.
-bool within(long long limit, std::initializer_list<long long> factors) {
-  long long p = 1;
-  for (long long f : factors) {
-    if (f != 0 && p > limit / f) return false;
-    p *= f;
-  }
-  return true;
-}
-
-// Writes must keep clear of every read and of each other.
-template <int NW, int NR>
-bool clash(const Range (&writes)[NW], const Range (&reads)[NR]) {
-  for (int i = 0; i < NW; ++i) {
-    if (overlaps_any(writes[i], reads, NR)) return true;
-    for (int j = i + 1; j < NW; ++j)
-      if (overlap(writes[i], writes[j])) return true;
-  }
-  return false;
-}
-
-Range range_or_none(const void* p, size_t bytes) { return p ? range_of(p, bytes) : Range{0, 0}; }
 
 // ---- short convolution ----------------------------------------------------
 
@@ -76,12 +45,9 @@ gdr::ConvArgs conv_args(const gdr_conv_dims& d, int T, gdr_act act, const void* 
   return a;
 }
 
-// Bytes from the first to behind the last element of rows `stride` apart.
-size_t rows_extent(size_t rows, int64_t stride, size_t width, size_t es) {
-  return rows ? ((rows - 1) * static_cast<size_t>(stride) + width) * es : 0;
-}
-
 // ---- selective state space scan --------------------------------------------
+
+bool supported_width(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
 int check_ssm_sizes(const gdr_ssm_dims* d, gdr_dtype io, int T) {
   if (!d) return GDR_E_NULL;

@@ -141,6 +141,56 @@ inline long long kv_touched_pages(int T, int page) {
 size_t attn_workspace_bytes(const KvArgs& a, int io_bf16);
 hipError_t launch_attn(const KvArgs& a, int io_bf16, hipStream_t stream);
 
+// Argument block of the norm and of the plain 8-bit rows.
+struct NormArgs {
+  const void* x;        // rows of H*D channels, x_stride elements apart
+  const void* gate;     // rows gate_stride apart, or nullptr
+  const float* weight;  // [H,D] or nullptr
+  void* residual;       // [R,H*D] or nullptr
+  void* y;              // [R,H*D] or nullptr
+  uint8_t* codes;       // [R,H*D] or nullptr
+  float* scales;        // [R,ceil(H*D/128)]
+  long long x_stride, gate_stride;
+  int R, H, D;
+  int res_bf16;         // dtype of the residual
+  int gate_first;       // the gate goes before the norm
+  int norm;             // 0: rows as they are
+  float eps;
+};
+constexpr int kNormMaxD = 32768;
+hipError_t launch_norm(const NormArgs& a, int io_bf16, hipStream_t stream);
+
+// Argument block of the 8-bit product.
+struct MatmulArgs {
+  const uint8_t* x;       // [M,K]
+  const float* x_scales;  // [M,ceil(K/128)]
+  const uint8_t* w;       // [N,K]
+  const float* w_scales;  // [ceil(N/128),ceil(K/128)]
+  const float* bias;      // [N] or nullptr
+  void* y;                // [M,N]
+  int M, N, K;
+};
+constexpr int kMatmulMaxK = 1 << 20;
+// Workgroups the finest of the product's tilings starts.
+long long matmul_max_grid(int M, int N);
+hipError_t launch_matmul(const MatmulArgs& a, int io_bf16, hipStream_t stream);
+
+// Argument block of the rotary positions.
+struct RopeArgs {
+  const void* x;       // rows of (H_q + 2 H_kv) D channels, x_stride elements apart
+  const double* freq;  // [R/2]
+  const int* pos;      // [B]
+  const int* lens;     // [B] or nullptr
+  void* q;
+  void* k;
+  void* v;             // or nullptr
+  long long x_stride;
+  int B, T, H_q, H_kv, D, R;
+  int interleaved;
+  float magnitude;
+};
+hipError_t launch_rope(const RopeArgs& a, int io_bf16, hipStream_t stream);
+
 // Workgroups a launch may have: 256 threads each within 32 bits of threads.
 constexpr long long kMaxGrid = (1ll << 24) - 1;
 

@@ -1,7 +1,7 @@
 /*
  * gdr.h -- C ABI of the gated delta rule library for AMD Instinct MI355X (gfx950).
  * The layers beside it (short convolution, state space scan, attention over an
- * 8-bit cache) follow in the second half.
+ * 8-bit cache; norms, 8-bit products, rotary positions) follow in the second half.
  *
  * The gated delta rule is the GatedDeltaNet linear-attention recurrence.  Per
  * batch row b and value head h it keeps a state S (dk x dv, fp32) and, for each
@@ -89,7 +89,8 @@ typedef enum gdr_status {
   GDR_E_NULL = -1,        /* a required pointer is NULL                         */
   GDR_E_SHAPE = -2,       /* negative size, H_v % H_qk != 0, H % G != 0, ...    */
   GDR_E_DTYPE = -3,       /* unknown io dtype, gate kind or activation          */
-  GDR_E_UNSUPPORTED = -4, /* dk/dv/chunk/W/N/P/D/page outside the compiled set  */
+  GDR_E_UNSUPPORTED = -4, /* dk/dv/chunk/W/N/P/D/page outside the compiled set, */
+                          /* or a value outside what an entry point takes       */
   GDR_E_WORKSPACE = -5,   /* workspace NULL or smaller than the size query      */
   GDR_E_HIP = -6,         /* the HIP runtime reported an error at launch        */
   GDR_E_ALIAS = -7,       /* o, the state or the workspace overlaps a buffer    */
@@ -425,6 +426,181 @@ int gdr_attn_cached(const gdr_kv_dims* dims, gdr_dtype io, const void* q, const 
                     const void* v_cache, const float* k_scale, const float* v_scale,
                     const int32_t* block_table, const int32_t* pos, const int32_t* lens, void* o,
                     float scale, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * What stands between the residual stream and the mixers above: the norm that a
+ * layer begins with, the 8-bit product that makes the packed row, rotary
+ * positions, and the norm or plain 8 bits on the way to the output's product.
+ *
+ * 8-bit rows: a row of K channels is K e4m3 codes (OCP, 448 at most, no
+ * infinity) and one fp32 scale for each block of 128 channels (the last block
+ * may be short); a code c stands for c * scale.
+ *
+ *     codes [R,K]    scales [R,ceil(K/128)]
+ *
+ * The library writes s = max(amax / 448, 2^-100), amax the largest finite
+ * magnitude of the block, and c = value / s rounded to nearest even; infinities
+ * become +-448, NaN stays NaN.  The product takes any scales.
+ * ------------------------------------------------------------------------ */
+
+/* R rows of H heads of D channels. */
+typedef struct gdr_norm_dims {
+  int32_t R, H, D;
+} gdr_norm_dims;
+
+/* Where the gate of gdr_rms_norm goes: behind the norm (the gated delta rule's
+ * output) or before it (the scan's). */
+typedef enum gdr_norm_gate {
+  GDR_NORM_GATE_NONE = 0,
+  GDR_NORM_GATE_AFTER = 1,
+  GDR_NORM_GATE_BEFORE = 2
+} gdr_norm_gate;
+
+/*
+ * gdr_rms_norm -- root-mean-square norm of rows, head by head:
+ *
+ *     h = x | x + residual | x silu(gate)     (nothing, a residual, a gate BEFORE)
+ *     y = h / sqrt(mean_D h^2 + eps) * weight [* silu(gate)]        (a gate AFTER)
+ *
+ * With a residual, h is stored back to it (rounded to its type; the norm takes
+ * h as summed in fp32).  H = 1 for whole rows.
+ *
+ *   dims      R, H, D.  D up to 32768; where H > 1, D is a multiple of 128 or
+ *             one of 16, 32, 64
+ *   io        dtype of x, gate and y
+ *   x         R rows of H*D channels, x_stride elements apart; aligned to its
+ *             element, and so is gate.  16-byte aligned rows and D a multiple of
+ *             8 take the wide path.
+ *   residual  [R,H*D] of dtype res, updated IN PLACE, or NULL (res is then
+ *             ignored); not together with a gate (GDR_E_UNSUPPORTED)
+ *   order     where the gate goes; gate and gate_stride are ignored for NONE
+ *   gate      R rows of H*D channels, gate_stride elements apart
+ *   weight    [H,D] fp32 or NULL (ones)
+ *   eps       finite and above 0, else GDR_E_UNSUPPORTED
+ *   y         [R,H*D] io dtype or NULL
+ *   codes, scales   8-bit rows of K = H*D channels, from y before it is rounded
+ *             to the io dtype; both or neither NULL, and not NULL together with y
+ *
+ * residual, y, codes and scales must not overlap each other or an input.  Sums
+ * of squares are 64-bit: rows of any finite fp32 magnitude have a finite norm
+ * (an h past fp32's range is infinite).
+ */
+int gdr_rms_norm(const gdr_norm_dims* dims, gdr_dtype io, const void* x, int64_t x_stride,
+                 gdr_dtype res, void* residual, gdr_norm_gate order, const void* gate,
+                 int64_t gate_stride, const float* weight, float eps, void* y, void* codes,
+                 float* scales, hipStream_t stream);
+
+/*
+ * gdr_quant_rows -- rows of H*D channels to 8-bit rows as they are (an
+ * attention's output has no norm before its product).  Arguments and conditions
+ * as in gdr_rms_norm.
+ */
+int gdr_quant_rows(const gdr_norm_dims* dims, gdr_dtype io, const void* x, int64_t x_stride,
+                   void* codes, float* scales, hipStream_t stream);
+
+typedef struct gdr_matmul_dims {
+  int32_t M, N, K;
+} gdr_matmul_dims;
+
+/*
+ * gdr_matmul_fp8 -- product of 8-bit rows with an 8-bit weight:
+ *
+ *     y[m,n] = bias[n] + sum_b x_scales[m,b] w_scales[n/128,b]
+ *                                sum_{k in block b} x[m,k] w[n,k]
+ *
+ * over blocks b of 128 channels.  Each block's sum is fp32, and so is the sum
+ * over blocks; y is rounded once.
+ *
+ *   dims      M rows, N outputs, K channels: K a multiple of 16, up to 2^20
+ *   io        dtype of y
+ *   x         [M,K] e4m3 codes, 16-byte aligned
+ *   x_scales  [M,ceil(K/128)] fp32
+ *   w         [N,K] e4m3 codes, 16-byte aligned
+ *   w_scales  [ceil(N/128),ceil(K/128)] fp32
+ *   bias      [N] fp32 or NULL
+ *   y         [M,N] io dtype; must not overlap an input
+ *   K == 0    y is the bias (zeros without one)
+ */
+int gdr_matmul_fp8(const gdr_matmul_dims* dims, gdr_dtype io, const void* x,
+                   const float* x_scales, const void* w, const float* w_scales,
+                   const float* bias, void* y, hipStream_t stream);
+
+/* Rows of B sequences of T tokens; H_q query heads and H_kv key and value heads
+ * of D channels, the first R of which are turned. */
+typedef struct gdr_rope_dims {
+  int32_t B, T, H_q, H_kv, D, R;
+} gdr_rope_dims;
+
+/* Which channels of a head's first R make a pair: (i, i + R/2) or (2i, 2i + 1). */
+typedef enum gdr_rope_pairs { GDR_ROPE_HALF = 0, GDR_ROPE_INTERLEAVED = 1 } gdr_rope_pairs;
+
+/*
+ * gdr_rope -- splits packed rows of q heads | k heads | v heads and turns q and k
+ * by their positions: pair i = (a, b) of token t of row b, at position
+ * p = pos[b] + t, becomes
+ *
+ *     magnitude * (a cos(p freq[i]) - b sin(p freq[i]),
+ *                  a sin(p freq[i]) + b cos(p freq[i]))
+ *
+ * The other channels are copied.  Outputs are as gdr_kv_append and
+ * gdr_attn_cached take them.  Angles are 64-bit: exact to 2^-24 of a turn at
+ * positions up to 2^24 and frequencies up to 1, and to 2^-20 at any position.
+ *
+ *   dims      B, T, H_q, H_kv, D (a multiple of 8 up to 512), R (even, 0 to D)
+ *   io        dtype of x, q, k and v
+ *   x         [B,T] rows of (H_q + 2 H_kv) D channels, x_stride elements apart;
+ *             aligned to its element.  16-byte aligned rows and pairs that fill
+ *             16 bytes (R a multiple of 8 or, in halves, of 16) take the wide path.
+ *   freq      [R/2] fp64 radians a position, finite (NULL if R is 0)
+ *   pos       [B] int32, the position of each row's first token
+ *   lens      [B] int32 or NULL
+ *   q, k, v   [B,T,H_q,D], [B,T,H_kv,D] twice, io dtype; v may be NULL (not
+ *             copied; x then has no v heads to show).  Not overlapping each
+ *             other or an input
+ */
+int gdr_rope(const gdr_rope_dims* dims, gdr_dtype io, gdr_rope_pairs pairs, const void* x,
+             int64_t x_stride, const double* freq, float magnitude, const int32_t* pos,
+             const int32_t* lens, void* q, void* k, void* v, hipStream_t stream);
+
+/* How frequencies base^(-2i/R) are stretched to contexts `factor` times as long
+ * as the `context` tokens that a model was trained on:
+ *
+ *   NONE    not at all
+ *   LINEAR  all by 1 / factor
+ *   BASE    by a larger base, base * factor^(R / (R - 2)): the first frequency
+ *           stays, the last is divided by factor
+ *   TURNS   by 1 / factor below `low` turns over the context, not at all above
+ *           `high`, and between by 1 / factor + u (1 - 1 / factor),
+ *           u = (turns - low) / (high - low)
+ *   INDEX   as TURNS, but u falls linearly in the index i, from 1 at the index
+ *           (rounded down, at least 0) that makes `high` turns to 0 at the one
+ *           (rounded up, at most R - 1) that makes `low`; the magnitude is
+ *           0.1 ln(factor) + 1 */
+typedef enum gdr_rope_kind {
+  GDR_ROPE_NONE = 0,
+  GDR_ROPE_LINEAR = 1,
+  GDR_ROPE_BASE = 2,
+  GDR_ROPE_TURNS = 3,
+  GDR_ROPE_INDEX = 4
+} gdr_rope_kind;
+
+typedef struct gdr_rope_scaling {
+  int32_t kind;  /* gdr_rope_kind */
+  double factor, context, low, high;
+} gdr_rope_scaling;
+
+/*
+ * gdr_rope_freqs -- the frequencies of gdr_rope, computed on the HOST into
+ * host memory (copy them to the device once).
+ *
+ *   R          even, 2 to 512
+ *   base       finite and above 1
+ *   scaling    NULL for none; factor >= 1; TURNS and INDEX: context > 0,
+ *              0 < low < high; BASE: R > 2.  Else GDR_E_UNSUPPORTED
+ *   freq       [R/2] written; magnitude (may be NULL) written
+ */
+int gdr_rope_freqs(int32_t R, double base, const gdr_rope_scaling* scaling, double* freq,
+                   float* magnitude);
 
 /* Static, human-readable text for a gdr_status value. */
 const char* gdr_strerror(int status);
