@@ -61,7 +61,9 @@ int check_matmul_sizes(const gdr_matmul_dims* d, gdr_dtype io) {
   if (!known_io(io)) return GDR_E_DTYPE;
   if (d->M < 0 || d->N < 0 || d->K < 0) return GDR_E_SHAPE;
   if (d->K % 16 != 0 || d->K > gdr::kMatmulMaxK) return GDR_E_UNSUPPORTED;
-  if (gdr::matmul_max_grid(d->M, d->N) > gdr::kMaxGrid) return GDR_E_SHAPE;
+  // The ends of the last tiles are 32-bit.
+  if (d->M > INT32_MAX - 256 || d->N > INT32_MAX - 256) return GDR_E_SHAPE;
+  if (gdr::matmul_grid(d->M, d->N, io == GDR_BF16) > gdr::kMaxGrid) return GDR_E_SHAPE;
   return GDR_OK;
 }
 

@@ -171,8 +171,8 @@ struct MatmulArgs {
   int M, N, K;
 };
 constexpr int kMatmulMaxK = 1 << 20;
-// Workgroups the finest of the product's tilings starts.
-long long matmul_max_grid(int M, int N);
+// Workgroups launch_matmul starts for these sizes.
+long long matmul_grid(int M, int N, int io_bf16);
 hipError_t launch_matmul(const MatmulArgs& a, int io_bf16, hipStream_t stream);
 
 // Argument block of the rotary positions.

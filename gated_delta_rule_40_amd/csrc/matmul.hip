@@ -17,6 +17,8 @@
 // stream_kernel: few rows.  The weight is read once, straight into registers; the
 // blocks of a row are shared by the waves of a workgroup and their sums joined in LDS.
 // Bound by HBM.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "gdr.h"
 #include "gdr_internal.h"
@@ -33,8 +35,8 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // Channels of 16 rows of one block as an operand: lane l holds row l % 16, channels
-// 32 (l / 16) ... + 31 (any order of the channels does, as long as it is the same for
-// both operands).  EXACT: widened to bf16.
+// 16 (l / 16) ... + 15 and 64 behind those (any order of the channels does, as long as
+// it is the same for both operands; in this one four lanes read 64 bytes in a row).  EXACT: widened to bf16.
 template <bool EXACT>
 struct Operand;
 template <>
@@ -78,13 +80,36 @@ __device__ __forceinline__ i32x8 join(i32x4 lo, i32x4 hi) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// 32 channels from k of a row of K, zeros behind its end (K a multiple of 16).
-__device__ __forceinline__ i32x8 load_channels(const uint8_t* row, int k, int K) {
-  const i32x4 zero = {0, 0, 0, 0};
-  const i32x4 lo = k < K ? *reinterpret_cast<const i32x4*>(row + k) : zero;
-  const i32x4 hi = k + 16 < K ? *reinterpret_cast<const i32x4*>(row + k + 16) : zero;
-  return join(lo, hi);
+// 16 bytes a lane from `base` (the same in every lane) + offset to LDS: lane l's go
+// to lds + 16 l.  Nothing waits for it here.  (m0, which takes the address in LDS, is
+// set by the compiler right before what needs it.)
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, unsigned offset, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(offset), "s"(base)
+               : "memory");
 }
+__device__ __forceinline__ void load_to_lds(const uint8_t* p, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds), "v"(p)
+               : "memory");
+}
+// 4 bytes a lane, lane l's to lds + 4 l.
+__device__ __forceinline__ void load_word_to_lds(const float* p, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(lds), "v"(p)
+               : "memory");
+}
+__device__ __forceinline__ unsigned lds_address(const void* p) {
+  return static_cast<unsigned>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// What lanes behind the last channel load.
+__device__ const uint4 kZeros = {0, 0, 0, 0};
 
 // Four neighbouring outputs of row m from column n.
 template <typename T>
@@ -105,52 +130,122 @@ __device__ __forceinline__ void store_out(const MatmulArgs& a, int m, int n, f32
   }
 }
 
+// Eight neighbouring outputs of row m from column n; `whole`: the columns are there, and
+// 16-byte aligned.  Plain stores: past the caches they are faster alone (4000 x 8192 x
+// 4096 156 against 168 us), but what reads the outputs next then takes longer (with the
+// convolution behind it 194 against 191 us, with plain 8-bit rows 187 against 183).
+template <typename T>
+__device__ __forceinline__ void store_out8(const MatmulArgs& a, int m, int n, f32x4 lo, f32x4 hi,
+                                           bool whole) {
+  if (m >= a.M) return;
+  T* y = static_cast<T*>(a.y) + static_cast<size_t>(m) * a.N + n;
+  if (whole) {
+    if (a.bias) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        lo[u] += a.bias[n + u];
+        hi[u] += a.bias[n + 4 + u];
+      }
+    }
+    T e[8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      e[u] = from_f32<T>(lo[u]);
+      e[4 + u] = from_f32<T>(hi[u]);
+    }
+#pragma unroll
+    for (int c = 0; c < static_cast<int>(sizeof(T)) / 2; ++c)
+      reinterpret_cast<uint4*>(y)[c] = reinterpret_cast<const uint4*>(e)[c];
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (n + u < a.N) {
+        const float v = u < 4 ? lo[u % 4] : hi[u % 4];
+        y[u] = from_f32<T>(v + (a.bias ? a.bias[n + u] : 0.0f));
+      }
+  }
+}
+
 // 16 NT outputs of 16 MT rows a workgroup; wave v takes the blocks v, v + WAVES, ...
+// It loads one straight into LDS, in a place of its own, while the products of the one
+// before run; nothing but the join at the end waits for other waves.  8 lanes bring a
+// row's 128 bytes: lanes that loaded their own operands touched 16 rows at once, four
+// times as many lines (64 rows 18.2 against 12.3 us, 16 rows with K = 14336 18.6 against
+// 11.5).  Two to four blocks ahead are no faster: the waves of a workgroup are enough.
 template <typename T, bool EXACT, int MT, int NT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void stream_kernel(MatmulArgs a, int row_tiles) {
-  __shared__ f32x4 part[WAVES][NT * MT][64];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  constexpr int kRows = 16 * (NT + MT), kPieces = kRows / 8;
+  constexpr int kPlace = kRows * kBlock + 256;  // the rows, then the scales of x
+  __shared__ __attribute__((aligned(1024))) uint8_t places[WAVES][kPlace];
+  static_assert(kPlace >= NT * MT * 1024, "the join takes the same place");
+  static_assert(MT <= 4, "one lane loads a row's scale");
+  const int lane = threadIdx.x % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int m0 = blockIdx.x % row_tiles * (16 * MT), n0 = blockIdx.x / row_tiles * (16 * NT);
   const int K = a.K, blocks = (K + kBlock - 1) / kBlock;
-  const int in = lane % 16, k0 = lane / 16 * 32;
+  const int in = lane % 16, g = lane / 16;
 
-  // Rows past the last are read as the last; their results are not stored.
-  const uint8_t* w[NT];
-  const uint8_t* x[MT];
-  const float* sx[MT];
+  // The weight's rows, then those of x; piece c of row r lies at c ^ (r % 8).  Rows past
+  // the last are read as the last; their results are not stored.
+  const uint8_t* wbase = a.w + static_cast<size_t>(n0) * K;
+  const uint8_t* xbase = a.x + static_cast<size_t>(m0) * K;
+  const int from = (lane % 8 ^ lane / 8) * 16;
+  unsigned offset[kPieces];
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-    w[i] = a.w + static_cast<size_t>(min(n0 + 16 * i + in, a.N - 1)) * K;
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const size_t m = min(m0 + 16 * j + in, a.M - 1);
-    x[j] = a.x + m * K;
-    sx[j] = a.x_scales + m * blocks;
+  for (int i = 0; i < kPieces; ++i) {
+    const int row = i * 8 + lane / 8;
+    const int r = i < 2 * NT ? min(row, a.N - 1 - n0) : min(row - 16 * NT, a.M - 1 - m0);
+    offset[i] = static_cast<unsigned>(r) * static_cast<unsigned>(K) + from;
   }
+  const float* sx = a.x_scales + static_cast<size_t>(min(m0 + lane % (16 * MT), a.M - 1)) * blocks;
   const float* sw = a.w_scales + static_cast<size_t>(n0 / kBlock) * blocks;
+  const uint8_t* place = places[wave];
+  const unsigned lds = lds_address(place);
+  auto fetch = [&](int b) {
+    const int k = b * kBlock;
+    if (k + kBlock <= K) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        load_to_lds((i < 2 * NT ? wbase : xbase) + k, offset[i], lds + i * 1024);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        load_to_lds(k + from < K ? (i < 2 * NT ? wbase : xbase) + k + offset[i]
+                                 : reinterpret_cast<const uint8_t*>(&kZeros),
+                    lds + i * 1024);
+    }
+    load_word_to_lds(sx + b, lds + kRows * kBlock);
+  };
+  if (wave < blocks) fetch(wave);
 
   f32x4 acc[NT][MT] = {};
+  const int p0 = (g ^ (in % 8)) * 16, p1 = p0 ^ 64;
   for (int b = wave; b < blocks; b += WAVES) {
-    const int k = b * kBlock + k0;
-    i32x8 wc[NT], xc[MT];
+    wait_loads();
+    auto operand = [&](int row) {
+      const uint8_t* p = place + (row + in) * kBlock;
+      Operand<EXACT> f;
+      f.set(join(*reinterpret_cast<const i32x4*>(p + p0), *reinterpret_cast<const i32x4*>(p + p1)));
+      return f;
+    };
+    Operand<EXACT> wf[NT], xf[MT];
     float s[MT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) wc[i] = load_channels(w[i], k, K);
+    for (int i = 0; i < NT; ++i) wf[i] = operand(16 * i);
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-      xc[j] = load_channels(x[j], k, K);
-      s[j] = sx[j][b] * sw[b];
+      xf[j] = operand(16 * (NT + j));
+      s[j] = *reinterpret_cast<const float*>(place + kRows * kBlock + (16 * j + in) * 4) * sw[b];
     }
-    Operand<EXACT> wf[NT], xf[MT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) wf[i].set(wc[i]);
-#pragma unroll
-    for (int j = 0; j < MT; ++j) xf[j].set(xc[j]);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // all read: the place is free
+    if (b + WAVES < blocks) fetch(b + WAVES);
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int j = 0; j < MT; ++j) acc[i][j] += block_product(wf[i], xf[j]) * s[j];
   }
+  __syncthreads();
+  f32x4(*part)[NT * MT][64] = reinterpret_cast<f32x4(*)[NT * MT][64]>(&places[0][0]);
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -182,25 +277,6 @@ hipError_t launch_stream(const MatmulArgs& a, hipStream_t stream) {
 // registers) while its products run.
 // ---------------------------------------------------------------------------
 
-// 16 bytes a lane from `base` (the same in every lane) + offset to LDS: lane l's go
-// to lds + 16 l.  Nothing waits for it here.
-__device__ __forceinline__ void load_to_lds(const uint8_t* base, unsigned offset, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :
-               : "s"(lds), "v"(offset), "s"(base)
-               : "memory");
-}
-__device__ __forceinline__ void load_to_lds(const uint8_t* p, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               :
-               : "s"(lds), "v"(p)
-               : "memory");
-}
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// What lanes behind the last channel load.
-__device__ const uint4 kZeros = {0, 0, 0, 0};
-
 // Workgroup `id` of `total` in the order in which workgroups that run together on one
 // XCD (every eighth) are neighbours.
 __device__ __forceinline__ int xcd_order(int id, int total) {
@@ -228,11 +304,19 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(MatmulArgs a, int ro
   const int m0 = (group * kRowGroup + within % tall) * BM, n0 = within / tall * BN;
   const int K = a.K, blocks = (K + kBlock - 1) / kBlock;
 
-  // Rows of 128 bytes; 16-byte piece c of row r lies at c ^ (r % 8), so that lanes
-  // that read one piece of many rows meet different banks.  A load of a wave fills 8
-  // rows: lane l brings piece (l % 8) ^ (l / 8) of row l / 8.  Rows past the last are
-  // read as the last; their results are not stored.
-  const int from = ((lane % 8) ^ (lane / 8)) * 16;
+  // Rows of 128 bytes, of which a load of a wave fills 8, lane l the 16 bytes at l % 8 of
+  // row l / 8.  Piece c of row r lies at c ^ key(r): the lanes that the LDS serves
+  // together (0-3, 12-15 and 20-27; 4-11, 16-19 and 28-31; the same from 32) then meet
+  // different banks, reading pieces g and g + 4 (lane 16 g + in) of the rows that
+  // `in` stands for.  Those are 16 neighbouring ones of x (key r % 8); of the weight
+  // 4 of every 8 out of 32, so that a lane holds 8 neighbouring outputs in a pair of
+  // products (key r % 4 + 4 (r / 8 % 2)).  Rows past the last are read as the last;
+  // their results are not stored.
+  auto piece = [&](int i) {  // of this lane's in load i, its first byte in the row
+    const int p = wave * kEach + i;  // rows 8 p ... 8 p + 7
+    const int key = p < BN / 8 ? lane / 8 % 4 + p % 2 * 4 : lane / 8;
+    return (lane % 8 ^ key) * 16;
+  };
   unsigned offset[kEach];
   const uint8_t* base[kEach];
 #pragma unroll
@@ -242,22 +326,26 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(MatmulArgs a, int ro
     const int r0 = w ? n0 : m0, last = (w ? a.N : a.M) - 1 - r0;
     base[i] = (w ? a.w : a.x) + static_cast<size_t>(r0) * K;
     offset[i] = static_cast<unsigned>(min((w ? row : row - BN) + lane / 8, last)) *
-                    static_cast<unsigned>(K) + from;
+                    static_cast<unsigned>(K) + piece(i);
   }
-  const unsigned lds0 = static_cast<unsigned>(
-      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void*)&tile[0][0]));
-  auto fetch = [&](int b) {
-    const unsigned lds = lds0 + (b & 1) * ((BN + BM) * kBlock) + wave * kEach * 1024;
+  const unsigned lds0 = lds_address(&tile[0][0]);
+  auto lds_of = [&](int b, int i) {
+    return lds0 + (b & 1) * ((BN + BM) * kBlock) + (wave * kEach + i) * 1024;
+  };
+  auto fetch = [&](int b, int i) {  // load i of this wave for block b, a whole one
+    load_to_lds(base[i] + b * kBlock, offset[i], lds_of(b, i));
+  };
+  auto fetch_all = [&](int b) {  // any block
     const int k = b * kBlock;
     if (k + kBlock <= K) {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) load_to_lds(base[i] + k, offset[i], lds + i * 1024);
+      for (int i = 0; i < kEach; ++i) fetch(b, i);
     } else {
-      const bool on = k + from < K;
 #pragma unroll
       for (int i = 0; i < kEach; ++i)
-        load_to_lds(on ? base[i] + k + offset[i] : reinterpret_cast<const uint8_t*>(&kZeros),
-                    lds + i * 1024);
+        load_to_lds(k + piece(i) < K ? base[i] + k + offset[i]
+                                     : reinterpret_cast<const uint8_t*>(&kZeros),
+                    lds_of(b, i));
     }
   };
 
@@ -270,39 +358,44 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(MatmulArgs a, int ro
   // A tile's columns past N may have no scale of their own.
   const float* sw =
       a.w_scales + static_cast<size_t>(min(n0 + wn, a.N - 1) / kBlock) * blocks;
-  const int p0 = ((2 * g) ^ (in % 8)) * 16, p1 = ((2 * g + 1) ^ (in % 8)) * 16;
+  const int p0 = (g ^ (in % 8)) * 16, p1 = p0 ^ 64;
 
-  // A vector load for the weight's scale, too: scalar ones would be waited for with the
-  // reads from LDS.
-  int zero = 0;
-  asm volatile("" : "+v"(zero));
+  // Scales are loaded for many blocks at once and handed out between lanes: of a row's,
+  // the four lanes that hold it take one of four blocks each, of the weight's each lane
+  // one of 64.  (One load a row and block touched a line for 4 bytes: 157 us without
+  // these loads against 192 with them.)
   float rs[MT], ws = 0.0f;
+  auto load_scales = [&](int b) {  // b a multiple of 4
 #pragma unroll
-  for (int j = 0; j < MT; ++j) rs[j] = 0.0f;
+    for (int j = 0; j < MT; ++j) rs[j] = sx[j][min(b + g, blocks - 1)];
+    if (b % 64 == 0) ws = sw[min(b + lane, blocks - 1)];
+  };
   if (blocks > 0) {
-#pragma unroll
-    for (int j = 0; j < MT; ++j) rs[j] = sx[j][0];
-    ws = sw[zero];
-    fetch(0);
+    load_scales(0);
+    fetch_all(0);
   }
   f32x4 acc[NT][MT] = {};
-  for (int b = 0; b < blocks; ++b) {
+  // One block; AHEAD: the next is there, and whole.
+  auto step = [&](int b, auto ahead) {
+    constexpr bool AHEAD = decltype(ahead)::value;
     wait_loads();
     __syncthreads();  // this block is in LDS, and no wave reads the one before
+    const float wb = __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws), b % 64));
     float s[MT];
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-      s[j] = rs[j] * ws;
+      s[j] = wb * __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(
+                                                (in + 16 * (b % 4)) * 4,
+                                                __builtin_bit_cast(int, rs[j])));
       asm volatile("" : "+v"(s[j]));  // here: a later use would wait for the loads below
     }
-    if (b + 1 < blocks) {
-      fetch(b + 1);
-#pragma unroll
-      for (int j = 0; j < MT; ++j) rs[j] = sx[j][b + 1];
-      ws = sw[b + 1 + zero];
+    if (AHEAD || b + 1 < blocks) {
+      if (b % 4 == 3) load_scales(b + 1);
+      if (!AHEAD) fetch_all(b + 1);
     }
 
-    const uint8_t* lw = tile[b & 1] + (wn + in) * kBlock;
+    const uint8_t* lw = tile[b & 1] + (wn + in / 4 * 8 + in % 4) * kBlock;
     const uint8_t* lx = tile[b & 1] + (BN + wm + in) * kBlock;
     auto operand = [&](const uint8_t* row) {
       Operand<EXACT> f;
@@ -313,6 +406,7 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(MatmulArgs a, int ro
     // A block's sum is scaled and added kLag products after its own, when it has left
     // the matrix pipe; the weight's operands are read one ahead.
     constexpr int kLag = 3;
+    static_assert(kEach <= NT * MT, "every load has its place");
     f32x4 sum[kLag + 1];
     Operand<EXACT> wf[2], xf[MT];
     wf[0] = operand(lw);
@@ -322,35 +416,33 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(MatmulArgs a, int ro
     for (int q = 0; q < NT * MT + kLag; ++q) {
       if (q < NT * MT) {
         const int i = q / MT, j = q % MT;
-        if (j == 0 && i + 1 < NT) wf[(i + 1) % 2] = operand(lw + (i + 1) * 16 * kBlock);
+        if (j == 0 && i + 1 < NT)
+          wf[(i + 1) % 2] = operand(lw + ((i + 1) / 2 * 32 + (i + 1) % 2 * 4) * kBlock);
         sum[q % (kLag + 1)] = block_product(wf[i % 2], xf[j]);
+        // The next block's loads, one behind each product: all at once they would hold
+        // the wave up until the memory pipe has taken them (161 against 154 us), later
+        // ones arrive late (156 to 163).
+        if (AHEAD && q < kEach) fetch(b + 1, q);
       }
-      if (q >= kLag) acc[(q - kLag) / MT][(q - kLag) % MT] += sum[(q - kLag) % (kLag + 1)] * s[(q - kLag) % MT];
+      if (q >= kLag) {
+        const int p = q - kLag;
+        acc[p / MT][p % MT] += sum[p % (kLag + 1)] * s[p % MT];
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
-  }
-  const int m = m0 + wm + in, n = n0 + wn + 4 * g;
-  if (m0 + BM <= a.M && n0 + BN <= a.N && a.N % 4 == 0) {
+  };
+  const int whole = K / kBlock;
+  int b = 0;
+  for (; b + 1 < whole; ++b) step(b, std::true_type{});
+  for (; b < blocks; ++b) step(b, std::false_type{});
+  // A lane holds 8 neighbouring outputs in a pair of products.
+  const int m = m0 + wm + in, n = n0 + wn + 8 * g;
+  const bool whole_row = n0 + BN <= a.N && a.N % (16 / static_cast<int>(sizeof(T))) == 0;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (a.bias) {
+  for (int i = 0; i < NT; i += 2)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) bias[u] = a.bias[n + 16 * i + u];
-      }
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const f32x4 v = acc[i][j] + bias;
-        store4<T>(static_cast<T*>(a.y) + static_cast<size_t>(m + 16 * j) * a.N + n + 16 * i, v[0],
-                  v[1], v[2], v[3]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < MT; ++j) store_out<T>(a, m + 16 * j, n + 16 * i, acc[i][j]);
-  }
+    for (int j = 0; j < MT; ++j)
+      store_out8<T>(a, m + 16 * j, n + 16 * i, acc[i][j], acc[i + 1][j], whole_row);
 }
 
 template <typename T, int WN, int WM, int NT, int MT>
@@ -364,24 +456,86 @@ hipError_t launch_tile(const MatmulArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Which kernel.  Up to 16 and 32 rows a tile of as many; past that the one with the
+// lowest estimate, in microseconds for K = 4096, of a fixed cost and one for each
+// round of 256 workgroups (fitted to 20 sizes from 64 x 8192 to 4000 x 8192; it picked
+// the fastest or one within 5%).  Measured at its edges, each time against the next:
+//   64 x 8192 stream 64 x 32 12.2, stream 64 x 64 14.3; 64 x 16384 21.4, 16.7
+//   192 x 8192 stream 64 x 32 27.6, tile 64 x 128 24.6
+//   512 x 8192 tile 64 x 128 32.8, tile 128 x 128 31.8
+//   1000 x 8192 tile 128 x 128 49.1, tile 256 x 128 45.5
+//   1500 x 8192 tile 128 x 128 73.7, tile 256 x 256 62.6; 2500 x 8192 118.8, 125.3
+// An fp32 output's operands take twice the registers: the two that would not fit are left
+// out, and the tiles' products take twice as long (1000 x 8192: 73.4 and 68.3).
+// ---------------------------------------------------------------------------
+enum class Plan { kOne, kTwo, kStream32, kStream64, kTile64, kTile128, kTile256, kTile256x256 };
+
+struct Option {
+  Plan plan;
+  int rows, cols;       // of a tile
+  float fixed, round;   // bf16 outputs
+  float fixed32, round32;
+};
+constexpr float kNever = 1e30f;
+constexpr Option kOptions[] = {
+    {Plan::kStream32, 64, 32, 5.0f, 7.2f, 5.0f, 7.2f},
+    {Plan::kStream64, 64, 64, 6.0f, 11.0f, 0.0f, kNever},
+    {Plan::kTile64, 64, 128, 10.0f, 12.0f, 14.0f, 16.5f},
+    {Plan::kTile128, 128, 128, 8.0f, 22.0f, 10.0f, 32.0f},
+    {Plan::kTile256, 256, 128, 2.0f, 43.0f, 0.0f, 68.0f},
+    {Plan::kTile256x256, 256, 256, 0.0f, 66.0f, 0.0f, kNever},
+};
+
+struct Choice {
+  Plan plan;
+  long long tiles;
+};
+long long tiles_of(int M, int N, int rows, int cols) {
+  return ((M + rows - 1ll) / rows) * ((N + cols - 1ll) / cols);
+}
+Choice choose(int M, int N, bool fp32) {
+  if (M <= 16) return Choice{Plan::kOne, tiles_of(M, N, 16, 16)};
+  if (M <= 32) return Choice{Plan::kTwo, tiles_of(M, N, 32, 32)};
+  Choice best = {};
+  float least = 0.0f;
+  for (const Option& o : kOptions) {
+    const long long tiles = tiles_of(M, N, o.rows, o.cols), rounds = (tiles + 255) / 256;
+    const float cost = (fp32 ? o.fixed32 : o.fixed) + (fp32 ? o.round32 : o.round) * rounds;
+    if (best.tiles == 0 || cost < least) {
+      best = Choice{o.plan, tiles};
+      least = cost;
+    }
+  }
+  return best;
+}
+
 template <typename T>
 hipError_t launch_io(const MatmulArgs& a, hipStream_t stream) {
-  if (a.M <= 16) return launch_stream<T, 1, 1, 8>(a, stream);
-  if (a.M <= 32) return launch_stream<T, 2, 1, 8>(a, stream);
-  if (a.M <= 256) return launch_stream<T, 4, 2, 8>(a, stream);
-  const long long big = ((a.M + 255ll) / 256) * ((a.N + 255ll) / 256);
-  // fp32: bf16 operands take twice the registers.
-  constexpr int kTall = sizeof(T) == 4 ? 4 : 8;
-  if (big >= 128) return launch_tile<T, 2, 4, kTall, 4>(a, stream);
-  return launch_tile<T, 2, 2, 4, 4>(a, stream);
+  switch (choose(a.M, a.N, sizeof(T) == 4).plan) {
+    case Plan::kOne:
+      // One block or two a wave: 1 x 8192, K = 4096 8.6 against 9.1 us with 8 waves; 16 x
+      // 4096, K = 14336 12.3 against 11.4.
+      return a.K <= 64 * kBlock ? launch_stream<T, 1, 1, 16>(a, stream)
+                                : launch_stream<T, 1, 1, 8>(a, stream);
+    case Plan::kTwo: return launch_stream<T, 2, 2, 8>(a, stream);
+    case Plan::kStream32: return launch_stream<T, 4, 2, 8>(a, stream);
+    case Plan::kTile64: return launch_tile<T, 2, 2, 4, 2>(a, stream);
+    case Plan::kTile128: return launch_tile<T, 2, 2, 4, 4>(a, stream);
+    case Plan::kTile256: return launch_tile<T, 2, 4, 4, 4>(a, stream);
+    case Plan::kStream64:
+      if constexpr (sizeof(T) == 2) return launch_stream<T, 4, 4, 8>(a, stream);
+      break;
+    case Plan::kTile256x256:
+      if constexpr (sizeof(T) == 2) return launch_tile<T, 2, 4, 8, 4>(a, stream);
+      break;
+  }
+  return hipErrorInvalidValue;  // an fp32 output is never given the last two
 }
 
 }  // namespace
 
-long long matmul_max_grid(int M, int N) {
-  const long long rows = (static_cast<long long>(M) + 15) / 16;
-  return rows * ((static_cast<long long>(N) + 15) / 16);
-}
+long long matmul_grid(int M, int N, int io_bf16) { return choose(M, N, !io_bf16).tiles; }
 
 hipError_t launch_matmul(const MatmulArgs& a, int io_bf16, hipStream_t stream) {
   return io_bf16 ? launch_io<bf16>(a, stream) : launch_io<float>(a, stream);

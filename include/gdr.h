@@ -511,7 +511,8 @@ typedef struct gdr_matmul_dims {
  * over blocks b of 128 channels.  Each block's sum is fp32, and so is the sum
  * over blocks; y is rounded once.
  *
- *   dims      M rows, N outputs, K channels: K a multiple of 16, up to 2^20
+ *   dims      M rows, N outputs (within 2^31 - 257), K channels: a multiple of 16, up
+ *             to 2^20
  *   io        dtype of y
  *   x         [M,K] e4m3 codes, 16-byte aligned
  *   x_scales  [M,ceil(K/128)] fp32

@@ -66,6 +66,19 @@ def test_products(M, N, K, io):
         check(inputs(M + N + K, M, N, K, bias), io_dtype(io))
 
 
+# Sizes that take each of the kernel's tilings, with whole and with ragged tiles.
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(16, 272, 1168), (32, 300, 656), (64, 8192, 272),
+                                   (100, 8192, 272), (97, 8184, 656), (192, 8192, 400),
+                                   (201, 8001, 144), (512, 8192, 272), (500, 8100, 528),
+                                   (1000, 8192, 272), (990, 8190, 400), (1536, 8192, 400),
+                                   (1500, 8001, 272), (1500, 8008, 1296)])
+def test_every_tiling(M, N, K, io):
+    require_gpu()
+    announce(f"matmul tiling M={M} N={N} K={K} io={io}")
+    check(inputs(M + N, M, N, K), io_dtype(io))
+
+
 @pytest.mark.parametrize("M,N,K", [(4000, 8192, 4096), (2047, 4100, 1040), (1, 8192, 14336),
                                    (64, 4096, 14336), (4097, 128, 4096), (5000, 16, 256),
                                    (16, 20000, 512)])

@@ -85,6 +85,7 @@ def matmul(m=5, n=300, k=272, io=1, x=A[0], sx=A[1], w=A[2], sw=A[3], bias=A[4],
 @pytest.mark.parametrize("case,expect", [
     (dict(dims=False), "NULL"), (dict(io=3), "DTYPE"), (dict(m=-1), "SHAPE"), (dict(n=-1), "SHAPE"),
     (dict(k=-16), "SHAPE"), (dict(m=2 ** 30, n=2 ** 20), "SHAPE"),
+    (dict(m=2 ** 31 - 1, n=1), "SHAPE"), (dict(m=1, n=2 ** 31 - 1), "SHAPE"),
     (dict(k=264), "UNSUPPORTED"), (dict(k=2 ** 20 + 16), "UNSUPPORTED"),
     (dict(x=None), "NULL"), (dict(sx=None), "NULL"), (dict(w=None), "NULL"),
     (dict(sw=None), "NULL"), (dict(y=None), "NULL"), (dict(k=0, y=None), "NULL"),
