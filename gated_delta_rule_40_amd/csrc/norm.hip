@@ -6,13 +6,14 @@
 // A value is read once, kept in registers over the sum, and written once: bound by
 // HBM, and by a launch and one chain of load, sum and store for few rows.  A thread
 // owns vectors of 8 neighbouring channels (16 lanes are a block of 128 channels), so
-// that a block's amax is a sum-like exchange inside 16 lanes.
+// that a block's amax is an exchange inside 16 lanes; all loads of a thread are under
+// way before the first is used.
 //
 // Heads of 16 to 512 channels (powers of two) lie within a wave: head_kernel, lanes
 // of many heads side by side, no barrier.  Others take a workgroup a head:
-// row_kernel, one barrier for the sum.  Inputs that are not 16-byte aligned are loaded
-// by elements (WIDE false); rows that are not of whole vectors take row_kernel with
-// one channel at a time, a wave's 64 lanes twice over a block.
+// row_kernel, one barrier for the sum.  Rows that are not 16-byte aligned (ALIGNED
+// false) are loaded and stored by the same vectors at any address, the last few
+// channels of a row that is not of whole vectors one by one.
 //
 // Squares are summed in 64 bits: they cannot overflow, and rsqrt(mean + eps) = m 2^e
 // is applied as h 2^e m, so rows of any finite magnitude keep their digits.
@@ -27,281 +28,335 @@ namespace {
 constexpr int kBlock = 128;           // channels that share a scale
 constexpr float kMinScale = 0x1p-100f;
 
-// Sum and maximum over the lanes that share lane / N (N a power of two up to 64).
+// x + y and max(x, y), y from the lane OFF further round a row of 16.
+template <int OFF>
+__device__ __forceinline__ unsigned rotated(unsigned x) {
+  return __builtin_amdgcn_update_dpp(0u, x, 0x120 + OFF, 0xf, 0xf, false);  // row_ror:OFF
+}
+template <int OFF>
+__device__ __forceinline__ double rotated(double x) {
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+  const unsigned lo = rotated<OFF>(static_cast<unsigned>(u));
+  const unsigned hi = rotated<OFF>(static_cast<unsigned>(u >> 32));
+  return __builtin_bit_cast(double, static_cast<unsigned long long>(hi) << 32 | lo);
+}
+
+// Sum over groups of N neighbouring lanes (N a power of two from 2 to 64).  Rotations
+// by 8, 4, 2, 1 leave every lane of a row of 16 with the row's sum; for less than 16
+// lanes, and across rows, lanes are exchanged through the LDS crossbar.
 template <int N>
 __device__ __forceinline__ double group_sum(double x) {
+  if constexpr (N < 16) {
 #pragma unroll
-  for (int o = 1; o < N; o *= 2) x += __shfl_xor(x, o, 64);
+    for (int o = 1; o < N; o *= 2) x += __shfl_xor(x, o, 64);
+  } else {
+    x += rotated<8>(x);
+    x += rotated<4>(x);
+    x += rotated<2>(x);
+    x += rotated<1>(x);
+#pragma unroll
+    for (int o = 16; o < N; o *= 2) x += __shfl_xor(x, o, 64);
+  }
   return x;
 }
-template <int N>
-__device__ __forceinline__ float group_max(float x) {
-#pragma unroll
-  for (int o = 1; o < N; o *= 2) x = fmaxf(x, __shfl_xor(x, o, 64));
-  return x;
+// Largest of a row of 16 lanes.
+__device__ __forceinline__ float row16_max(float x) {
+  auto with = [](float v, unsigned r) { return fmaxf(v, __builtin_bit_cast(float, r)); };
+  x = with(x, rotated<8>(__builtin_bit_cast(unsigned, x)));
+  x = with(x, rotated<4>(__builtin_bit_cast(unsigned, x)));
+  x = with(x, rotated<2>(__builtin_bit_cast(unsigned, x)));
+  return with(x, rotated<1>(__builtin_bit_cast(unsigned, x)));
 }
 
 // 1 / sqrt(ss / n + eps) = m * p, p a power of two (exact also where fp32 holds it
-// only as a subnormal).
+// only as a subnormal).  The hardware's root is good to 2^-23; one step of Newton's
+// method doubles the digits.
 struct Root {
   float m, p;
 };
-__device__ __forceinline__ Root inverse_root(double ss, int n, float eps) {
-  const double r = 1.0 / sqrt(ss / n + static_cast<double>(eps));
-  int e = 0;
-  const double m = frexp(r, &e);
-  return Root{static_cast<float>(m), ldexpf(1.0f, e)};
+__device__ __forceinline__ Root inverse_root(double ss, double inverse_n, float eps) {
+  const double v = ss * inverse_n + static_cast<double>(eps);
+  double r = __builtin_amdgcn_rsq(v);
+  r = __builtin_fma(0.5 * r, __builtin_fma(-v * r, r, 1.0), r);
+  return Root{static_cast<float>(__builtin_amdgcn_frexp_mant(r)),
+              ldexpf(1.0f, __builtin_amdgcn_frexp_exp(r))};
 }
 
-// The scale of a block and its inverse.
-__device__ __forceinline__ float block_scale(float amax) {
-  return fmaxf(amax * (1.0f / kE4m3Max), kMinScale);
-}
+// Eight neighbouring values in memory.
+template <typename T>
+struct Vec {
+  T e[8];
+};
+template <typename T>
+struct __attribute__((packed, aligned(1))) AnyVec {
+  T e[8];
+};
 
-template <typename T, int VEC, bool WIDE = true>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1 || !WIDE) {
+// `n` of them are there (8 where rows are ALIGNED).
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ Vec<T> load_vec(const T* p, int n) {
+  Vec<T> v;
+  if constexpr (ALIGNED) {
 #pragma unroll
-    for (int u = 0; u < VEC; ++u) v[u] = to_f32(p[u]);
+    for (int c = 0; c < static_cast<int>(sizeof(T)) / 2; ++c) {
+      const uint4 w = reinterpret_cast<const uint4*>(p)[c];
+      __builtin_memcpy(&v.e[c * (16 / sizeof(T))], &w, 16);
+    }
+  } else if (n >= 8) {
+    const AnyVec<T> a = *reinterpret_cast<const AnyVec<T>*>(p);
+    __builtin_memcpy(&v, &a, sizeof(v));
   } else {
-    load_row<T, VEC>(p, v);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v.e[u] = u < n ? p[u] : from_f32<T>(0.0f);
+  }
+  return v;
+}
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void store_vec(T* p, const float (&x)[8], int n) {
+  Vec<T> v;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) v.e[u] = from_f32<T>(x[u]);
+  if constexpr (ALIGNED) {
+#pragma unroll
+    for (int c = 0; c < static_cast<int>(sizeof(T)) / 2; ++c) {
+      uint4 w;
+      __builtin_memcpy(&w, &v.e[c * (16 / sizeof(T))], 16);
+      reinterpret_cast<uint4*>(p)[c] = w;
+    }
+  } else if (n >= 8) {
+    AnyVec<T> a;
+    __builtin_memcpy(&a, &v, sizeof(v));
+    *reinterpret_cast<AnyVec<T>*>(p) = a;
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (u < n) p[u] = v.e[u];
   }
 }
-
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    *p = from_f32<T>(v[0]);
-  } else {
-    T e[VEC];
-#pragma unroll
-    for (int u = 0; u < VEC; ++u) e[u] = from_f32<T>(v[u]);
-#pragma unroll
-    for (int c = 0; c < VEC * static_cast<int>(sizeof(T)) / 16; ++c)
-      reinterpret_cast<uint4*>(p)[c] = reinterpret_cast<const uint4*>(e)[c];
-  }
-}
-
-__device__ __forceinline__ void store_codes8(uint8_t* p, const float (&v)[8], float inv) {
+template <bool ALIGNED>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[8], float inv, int n) {
   uint2 w;
   w.x = e4m3_pair(v[0] * inv, v[1] * inv) | e4m3_pair(v[2] * inv, v[3] * inv) << 16;
   w.y = e4m3_pair(v[4] * inv, v[5] * inv) | e4m3_pair(v[6] * inv, v[7] * inv) << 16;
-  *reinterpret_cast<uint2*>(p) = w;
-}
-
-// h of VEC channels from `at` of a row (x, gate) or of the dense tensors
-// (residual, which takes h).  g: silu of the gate where it comes after the norm.
-template <typename T, int VEC, bool WIDE>
-__device__ __forceinline__ void form_h(const NormArgs& a, size_t row, size_t col, float (&h)[VEC],
-                                       float (&g)[VEC]) {
-  load_vec<T, VEC, WIDE>(static_cast<const T*>(a.x) + row * a.x_stride + col, h);
-  if (a.residual) {
-    const size_t at = row * (static_cast<size_t>(a.H) * a.D) + col;
-    float r[VEC];
-    if (a.res_bf16) {
-      bf16* p = static_cast<bf16*>(a.residual) + at;
-      load_vec<bf16, VEC>(p, r);
+  if constexpr (ALIGNED) {
+    *reinterpret_cast<uint2*>(p) = w;
+  } else if (n >= 8) {
+    AnyVec<uint8_t> a;
+    __builtin_memcpy(&a, &w, 8);
+    *reinterpret_cast<AnyVec<uint8_t>*>(p) = a;
+  } else {
 #pragma unroll
-      for (int u = 0; u < VEC; ++u) h[u] += r[u];
-      store_vec<bf16, VEC>(p, h);
-    } else {
-      float* p = static_cast<float*>(a.residual) + at;
-      load_vec<float, VEC>(p, r);
-#pragma unroll
-      for (int u = 0; u < VEC; ++u) h[u] += r[u];
-      store_vec<float, VEC>(p, h);
-    }
-  }
-  if (a.gate) {
-    load_vec<T, VEC, WIDE>(static_cast<const T*>(a.gate) + row * a.gate_stride + col, g);
-#pragma unroll
-    for (int u = 0; u < VEC; ++u) g[u] = silu_hw(g[u]);
-    if (a.gate_first) {
-#pragma unroll
-      for (int u = 0; u < VEC; ++u) h[u] *= g[u];
-    }
+    for (int u = 0; u < 8; ++u)
+      if (u < n) p[u] = static_cast<uint8_t>((u < 4 ? w.x : w.y) >> u % 4 * 8);
   }
 }
 
-// y of VEC channels; w points at their weights.
-template <int VEC, bool WIDE>
-__device__ __forceinline__ void form_y(const NormArgs& a, Root r, const float* w, float (&h)[VEC],
-                                       const float (&g)[VEC]) {
-#pragma unroll
-  for (int u = 0; u < VEC; ++u) h[u] = h[u] * r.p * r.m;
-  if (w) {
-    float wt[VEC];
-    load_vec<float, VEC, WIDE>(w, wt);
-#pragma unroll
-    for (int u = 0; u < VEC; ++u) h[u] *= wt[u];
-  }
-  if (a.gate && !a.gate_first) {
-#pragma unroll
-    for (int u = 0; u < VEC; ++u) h[u] *= g[u];
-  }
-}
+// A thread's vectors: where they lie, and their values on the way from x to y.
+template <typename T, bool ALIGNED, int NV>
+struct Vectors {
+  size_t row[NV];
+  int col[NV];   // in the row
+  int n[NV];     // channels that are there; 0: nothing
+  float h[NV][8];
+  Vec<T> z[NV];  // the gate, where it comes after the norm
 
-// LANES lanes a head (of 8 LANES channels).  Every row is padded to whole blocks of
-// 128 channels with lanes that have nothing, so that 16 lanes are a block.
-template <typename T, int LANES, bool WIDE>
-__global__ __launch_bounds__(256) void head_kernel(NormArgs a, unsigned slots) {
-  const unsigned idx = blockIdx.x * 256u + threadIdx.x;  // rows times slots are within 2^30
-  const size_t row = idx / slots;
-  const unsigned slot = idx % slots;
-  const int W = a.H * a.D;
-  const bool on = row < static_cast<size_t>(a.R) && slot * 8 < static_cast<unsigned>(W);
-  float h[8] = {}, g[8] = {};
-  if (on) form_h<T, 8, WIDE>(a, row, slot * 8, h, g);
-  if (a.norm) {
-    double ss = 0.0;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) ss += static_cast<double>(h[u]) * h[u];
-    const Root r = inverse_root(group_sum<LANES>(ss), a.D, a.eps);
-    if (on) form_y<8, WIDE>(a, r, a.weight ? a.weight + slot * 8 : nullptr, h, g);
-  }
-  if (on && a.y) store_vec<T, 8>(static_cast<T*>(a.y) + row * W + slot * 8, h);
-  if (a.codes) {
-    float top = 0.0f;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) top = fmaxf(top, finite_abs(h[u]));
-    const float s = block_scale(group_max<16>(top));
-    if (on) {
-      store_codes8(a.codes + row * W + slot * 8, h, 1.0f / s);
-      if (slot % 16 == 0) a.scales[row * (slots / 16) + slot / 16] = s;
-    }
-  }
-}
-
-// A workgroup of NT threads for each (row, head), NV vectors of VEC channels a thread.
-template <typename T, int VEC, int NT, int NV, bool WIDE>
-__global__ __launch_bounds__(NT) void row_kernel(NormArgs a) {
-  constexpr int NW = NT / 64;
-  static_assert(VEC == 8 || NV % 2 == 0, "a wave's lanes go twice over a block");
-  const size_t row = blockIdx.x / a.H;
-  const int head = blockIdx.x % a.H, D = a.D;
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const size_t W = static_cast<size_t>(a.H) * D, col0 = static_cast<size_t>(head) * D;
-  // Channel of a thread's vector j within the head.
-  auto channel = [&](int j) {
-    if constexpr (VEC == 8) return (j * NT + static_cast<int>(threadIdx.x)) * 8;
-    return ((j / 2) * NW + wave) * kBlock + (j % 2) * 64 + lane;
-  };
-  float h[NV][VEC], g[NV][VEC];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = channel(j);
-#pragma unroll
-    for (int u = 0; u < VEC; ++u) h[j][u] = g[j][u] = 0.0f;
-    if (c < D) form_h<T, VEC, WIDE>(a, row, col0 + c, h[j], g[j]);
-  }
-  if (a.norm) {
-    double ss = 0.0;
+  // h, and the residual's new values.
+  __device__ __forceinline__ void load(const NormArgs& a, int W) {
+    Vec<T> x[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
+      if (n[j] > 0)
+        x[j] = load_vec<T, ALIGNED>(static_cast<const T*>(a.x) + row[j] * a.x_stride + col[j], n[j]);
+    if (a.gate) {
 #pragma unroll
-      for (int u = 0; u < VEC; ++u) ss += static_cast<double>(h[j][u]) * h[j][u];
-    ss = group_sum<64>(ss);
-    if constexpr (NW > 1) {
-      __shared__ double part[NW];
-      if (lane == 0) part[wave] = ss;
-      __syncthreads();
-      ss = 0.0;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) ss += part[w];
+      for (int j = 0; j < NV; ++j)
+        if (n[j] > 0)
+          z[j] = load_vec<T, ALIGNED>(
+              static_cast<const T*>(a.gate) + row[j] * a.gate_stride + col[j], n[j]);
     }
-    const Root r = inverse_root(ss, D, a.eps);
+    if (a.residual) {
+      if (a.res_bf16)
+        add<bf16>(a, W, x);
+      else
+        add<float>(a, W, x);
+    } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = channel(j);
-      if (c < D) form_y<VEC, WIDE>(a, r, a.weight ? a.weight + col0 + c : nullptr, h[j], g[j]);
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          h[j][u] = n[j] > 0 ? to_f32(x[j].e[u]) : 0.0f;
+          if (a.gate && a.gate_first && n[j] > 0) h[j][u] *= silu_hw(to_f32(z[j].e[u]));
+        }
     }
   }
-  if (a.y) {
+  template <typename R>
+  __device__ __forceinline__ void add(const NormArgs& a, int W, const Vec<T> (&x)[NV]) {
+    R* residual = static_cast<R*>(a.residual);
+    Vec<R> r[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (n[j] > 0) r[j] = load_vec<R, ALIGNED>(residual + row[j] * W + col[j], n[j]);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = channel(j);
-      if (c < D) store_vec<T, VEC>(static_cast<T*>(a.y) + row * W + col0 + c, h[j]);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) h[j][u] = n[j] > 0 ? to_f32(x[j].e[u]) + to_f32(r[j].e[u]) : 0.0f;
+      if (n[j] > 0) store_vec<R, ALIGNED>(residual + row[j] * W + col[j], h[j], n[j]);
     }
   }
-  if (!a.codes) return;
-  float* scales = a.scales + row * ((W + kBlock - 1) / kBlock) + col0 / kBlock;
-  uint8_t* codes = a.codes + row * W + col0;
-  if constexpr (VEC == 8) {
+  __device__ __forceinline__ double squares(int j) const {
+    double ss = 0.0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) ss = __builtin_fma(static_cast<double>(h[j][u]), h[j][u], ss);
+    return ss;
+  }
+  // y in h's place; w: the weights of vector j, or nullptr.
+  __device__ __forceinline__ void scale(const NormArgs& a, int j, Root r, const Vec<float>* w) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      h[j][u] = h[j][u] * r.p * r.m;
+      if (w) h[j][u] *= w->e[u];
+      if (a.gate && !a.gate_first) h[j][u] *= silu_hw(to_f32(z[j].e[u]));
+    }
+  }
+  __device__ __forceinline__ void store(const NormArgs& a, int W) const {
+    if (a.y) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (n[j] > 0) store_vec<T, ALIGNED>(static_cast<T*>(a.y) + row[j] * W + col[j], h[j], n[j]);
+    }
+    if (!a.codes) return;
+    const size_t blocks = (static_cast<size_t>(W) + kBlock - 1) / kBlock;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = channel(j);
       float top = 0.0f;
 #pragma unroll
       for (int u = 0; u < 8; ++u) top = fmaxf(top, finite_abs(h[j][u]));
-      const float s = block_scale(group_max<16>(top));
-      if (c < D) {
-        store_codes8(codes + c, h[j], 1.0f / s);
-        if (lane % 16 == 0) scales[c / kBlock] = s;
+      const float s = fmaxf(row16_max(top) * (1.0f / kE4m3Max), kMinScale);
+      if (n[j] > 0) {
+        store_codes<ALIGNED>(a.codes + row[j] * W + col[j], h[j], 1.0f / s, n[j]);
+        if (threadIdx.x % 16 == 0) a.scales[row[j] * blocks + col[j] / kBlock] = s;
       }
     }
-  } else {
+  }
+};
+
+// LANES lanes a head (of 8 LANES channels).  Every row is padded to whole blocks of
+// 128 channels with lanes that have nothing, so that 16 lanes are a block.
+template <typename T, bool ALIGNED, int LANES>
+__global__ __launch_bounds__(256) void head_kernel(NormArgs a, unsigned slots, double inverse_n) {
+  const int W = a.H * a.D;
+  const unsigned idx = blockIdx.x * 256u + threadIdx.x;  // within 2^30
+  Vectors<T, ALIGNED, 1> v;
+  v.row[0] = idx / slots;
+  v.col[0] = idx % slots * 8;
+  v.n[0] = v.row[0] < static_cast<size_t>(a.R) && v.col[0] < W ? 8 : 0;
+  Vec<float> w;
+  if (a.weight && v.n[0] > 0) w = load_vec<float, ALIGNED>(a.weight + v.col[0], 8);
+  v.load(a, W);
+  if (a.norm) {
+    const Root r = inverse_root(group_sum<LANES>(v.squares(0)), inverse_n, a.eps);
+    v.scale(a, 0, r, a.weight ? &w : nullptr);
+  }
+  v.store(a, W);
+}
+
+// A workgroup of NT threads for each (row, head), NV vectors a thread.
+template <typename T, bool ALIGNED, int NT, int NV>
+__global__ __launch_bounds__(NT) void row_kernel(NormArgs a, double inverse_n) {
+  constexpr int NW = NT / 64;
+  const size_t row = blockIdx.x / a.H;
+  const int first = blockIdx.x % a.H * a.D, D = a.D, W = a.H * D;
+  Vectors<T, ALIGNED, NV> v;
 #pragma unroll
-    for (int j = 0; j < NV; j += 2) {
-      const int c = channel(j);
-      const float s = block_scale(
-          group_max<64>(fmaxf(finite_abs(h[j][0]), finite_abs(h[j + 1][0]))));
-      const unsigned pair = e4m3_pair(h[j][0] * (1.0f / s), h[j + 1][0] * (1.0f / s));
-      if (c < D) codes[c] = static_cast<uint8_t>(pair);
-      if (c + 64 < D) codes[c + 64] = static_cast<uint8_t>(pair >> 8);
-      if (lane == 0 && c < D) scales[c / kBlock] = s;
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * NT + static_cast<int>(threadIdx.x)) * 8;
+    v.row[j] = row;
+    v.col[j] = first + c;
+    v.n[j] = D - c;
+  }
+  constexpr bool kEarly = NV <= 2;  // weights with the rest; four vectors' would spill
+  Vec<float> w[NV];
+  auto weights = [&](int j) {
+    if (v.n[j] > 0) w[j] = load_vec<float, ALIGNED>(a.weight + v.col[j], v.n[j]);
+  };
+  if (kEarly && a.weight) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) weights(j);
+  }
+  v.load(a, W);
+  if (a.norm) {
+    double ss = 0.0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) ss += v.squares(j);
+    ss = group_sum<64>(ss);
+    if constexpr (NW > 1) {
+      __shared__ double part[NW];
+      if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = ss;
+      __syncthreads();
+      ss = 0.0;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) ss += part[i];
+    }
+    const Root r = inverse_root(ss, inverse_n, a.eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!kEarly && a.weight) weights(j);
+      v.scale(a, j, r, a.weight ? &w[j] : nullptr);
     }
   }
+  v.store(a, W);
 }
 
-template <typename T, int LANES, bool WIDE>
+template <typename T, bool ALIGNED, int LANES>
 hipError_t launch_heads(const NormArgs& a, hipStream_t stream) {
   const unsigned slots = (a.H * a.D + kBlock - 1) / kBlock * 16;
-  const unsigned threads = static_cast<unsigned>(a.R) * slots;
-  hipLaunchKernelGGL((head_kernel<T, LANES, WIDE>), dim3((threads + 255) / 256), dim3(256), 0,
-                     stream, a, slots);
+  const unsigned vectors = static_cast<unsigned>(a.R) * slots;
+  hipLaunchKernelGGL((head_kernel<T, ALIGNED, LANES>), dim3((vectors + 255) / 256), dim3(256), 0,
+                     stream, a, slots, 1.0 / a.D);
   return hipGetLastError();
 }
 
-template <typename T, int VEC, int NT, int NV, bool WIDE>
+template <typename T, bool ALIGNED, int NT, int NV>
 hipError_t launch_rows(const NormArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((row_kernel<T, VEC, NT, NV, WIDE>),
-                     dim3(static_cast<unsigned>(a.R) * a.H), dim3(NT), 0, stream, a);
+  hipLaunchKernelGGL((row_kernel<T, ALIGNED, NT, NV>), dim3(static_cast<unsigned>(a.R) * a.H),
+                     dim3(NT), 0, stream, a, 1.0 / a.D);
   return hipGetLastError();
 }
 
-template <typename T, bool WIDE>
-hipError_t launch_vectors(const NormArgs& a, hipStream_t stream) {
+template <typename T, bool ALIGNED>
+hipError_t launch_sizes(const NormArgs& a, hipStream_t stream) {
   switch (a.D) {
-    case 16: return launch_heads<T, 2, WIDE>(a, stream);
-    case 32: return launch_heads<T, 4, WIDE>(a, stream);
-    case 64: return launch_heads<T, 8, WIDE>(a, stream);
-    case 128: return launch_heads<T, 16, WIDE>(a, stream);
-    case 256: return launch_heads<T, 32, WIDE>(a, stream);
-    case 512: return launch_heads<T, 64, WIDE>(a, stream);
+    case 16: return launch_heads<T, ALIGNED, 2>(a, stream);
+    case 32: return launch_heads<T, ALIGNED, 4>(a, stream);
+    case 64: return launch_heads<T, ALIGNED, 8>(a, stream);
+    case 128: return launch_heads<T, ALIGNED, 16>(a, stream);
+    case 256: return launch_heads<T, ALIGNED, 32>(a, stream);
+    case 512: return launch_heads<T, ALIGNED, 64>(a, stream);
     default: break;
   }
-  if (a.D <= 512) return launch_rows<T, 8, 64, 1, WIDE>(a, stream);
-  if (a.D <= 2048) return launch_rows<T, 8, 256, 1, WIDE>(a, stream);
-  if (a.D <= 4096) return launch_rows<T, 8, 256, 2, WIDE>(a, stream);
-  if (a.D <= 8192) return launch_rows<T, 8, 256, 4, WIDE>(a, stream);
-  return launch_rows<T, 8, 1024, 4, WIDE>(a, stream);
+  // One vector a thread for few rows, two to four where rows fill the GPU.
+  const bool few = static_cast<long long>(a.R) * a.H < 1024;
+  if (a.D <= 512) return launch_rows<T, ALIGNED, 64, 1>(a, stream);
+  if (a.D <= 2048) return launch_rows<T, ALIGNED, 256, 1>(a, stream);
+  if (a.D <= 4096)
+    return few ? launch_rows<T, ALIGNED, 512, 1>(a, stream)
+               : launch_rows<T, ALIGNED, 256, 2>(a, stream);
+  if (a.D <= 8192)
+    return few ? launch_rows<T, ALIGNED, 1024, 1>(a, stream)
+               : launch_rows<T, ALIGNED, 256, 4>(a, stream);
+  return launch_rows<T, ALIGNED, 1024, 4>(a, stream);
 }
 
 template <typename T>
 hipError_t launch_io(const NormArgs& a, hipStream_t stream) {
-  if (a.D % 8 != 0) {  // H = 1
-    if (a.D <= 512) return launch_rows<T, 1, 64, 8, false>(a, stream);
-    if (a.D <= 4096) return launch_rows<T, 1, 256, 16, false>(a, stream);
-    return launch_rows<T, 1, 1024, 32, false>(a, stream);
-  }
   constexpr int kPer = 16 / static_cast<int>(sizeof(T));
   auto rows_aligned = [&](const void* p, long long stride) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (stride % kPer == 0 || a.R == 1);
   };
-  const bool wide = rows_aligned(a.x, a.x_stride) &&
-                    (!a.gate || rows_aligned(a.gate, a.gate_stride)) &&
-                    reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
-  return wide ? launch_vectors<T, true>(a, stream) : launch_vectors<T, false>(a, stream);
+  const bool aligned = a.D % 8 == 0 && rows_aligned(a.x, a.x_stride) &&
+                       (!a.gate || rows_aligned(a.gate, a.gate_stride)) &&
+                       reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
+  return aligned ? launch_sizes<T, true>(a, stream) : launch_sizes<T, false>(a, stream);
 }
 
 }  // namespace
