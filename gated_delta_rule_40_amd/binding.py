@@ -513,13 +513,14 @@ def gdr_attn_cached(q, k_cache, v_cache, k_scale, v_scale, block_table, pos, o, 
             _ptr(o, "o", (B, T, H_q, D), q.dtype, dev), float(scale), ws, ws_bytes)
 
 
-def _rows(t, name):
-    """Sizes, dtype code, device and row stride of rows [R,W] whose channels are
-    contiguous (the rows may lie apart, as in a slice of a wider row)."""
-    (R, W), io, dev = _lead(t, name, 2)
+def _apart(t, name, R, W):
+    """Row stride of rows [R,W] whose channels are contiguous (the rows may lie apart,
+    as in a slice of a wider row)."""
+    if t.is_contiguous():
+        return W
     if t.stride(1) != 1 and W > 1:
         raise ValueError(f"{name}'s channels must be contiguous")
-    return R, W, io, dev, t.stride(0) if R > 1 else W
+    return t.stride(0) if R > 1 else W
 
 
 def _f8_rows(codes, scales, R, W, dev):
@@ -528,10 +529,10 @@ def _f8_rows(codes, scales, R, W, dev):
         if scales is not None:
             raise ValueError("scales without codes")
         return None, None
-    if getattr(codes, "dtype", None) not in _F8:
+    if not isinstance(codes, torch.Tensor) or codes.dtype not in _F8:
         raise ValueError("codes must be a float8_e4m3fn or uint8 tensor")
     return (_ptr(codes, "codes", (R, W), codes.dtype, dev),
-            _ptr(scales, "scales", (R, -(-W // 128)), _F32, dev))
+            _ptr(scales, "scales", (R, (W + 127) // 128), _F32, dev))
 
 
 def gdr_rms_norm(x, weight=None, y=None, codes=None, scales=None, *, residual=None, gate=None,
@@ -543,44 +544,47 @@ def gdr_rms_norm(x, weight=None, y=None, codes=None, scales=None, *, residual=No
     multiplies the result, or x with gate_first).  Outputs: y [R,H*D] in x's dtype,
     codes [R,H*D] (float8_e4m3fn or uint8) with scales [R,ceil(H*D/128)] fp32, or
     both."""
-    R, W, io, dev, row = _rows(x, "x")
-    H = 1 if heads is None else heads
-    w = None
+    (R, W), io, dev = _lead(x, "x", 2)
+    row, dtype, H, w = _apart(x, "x", R, W), x.dtype, heads, None
     if weight is not None:
-        if not isinstance(weight, torch.Tensor) or weight.dim() not in (1, 2):
+        shape = weight.shape if isinstance(weight, torch.Tensor) else ()
+        if len(shape) not in (1, 2):
             raise ValueError("weight must be a tensor [H,D] or [D]")
-        shape = weight.shape
         H = shape[0] if len(shape) == 2 else 1
         if heads is not None and heads != H:
             raise ValueError(f"weight has {H} heads, expected {heads}")
-        w = _ptr(weight, "weight", (H, W // H) if len(shape) == 2 and H else (W,), _F32, dev)
+    elif H is None:
+        H = 1
     if H < 1 or W % H:
         raise ValueError(f"{W} channels are not {H} heads")
-    res, r = 0, None
+    if weight is not None:
+        w = _ptr(weight, "weight", (H, W // H) if len(shape) == 2 else (W,), _F32, dev)
+    res, r, order, g, g_row = 0, None, GDR_NORM_GATE_NONE, None, 0
     if residual is not None:
         res = _io_code(getattr(residual, "dtype", None))
         r = _ptr(residual, "residual", (R, W), residual.dtype, dev)
-    order, g, g_row = GDR_NORM_GATE_NONE, None, 0
     if gate is not None:
-        gr, gw, _, g_dev, g_row = _rows(gate, "gate")
-        if (gr, gw) != (R, W) or gate.dtype != x.dtype or g_dev != dev:
-            raise ValueError(f"gate must be like x: [{R},{W}], {x.dtype}, {dev}")
+        shape, _, g_dev = _lead(gate, "gate", 2)
+        if shape != x.shape or gate.dtype != dtype or g_dev != dev:
+            raise ValueError(f"gate must be like x: [{R},{W}], {dtype}, {dev}")
         order, g = GDR_NORM_GATE_BEFORE if gate_first else GDR_NORM_GATE_AFTER, gate.data_ptr()
+        g_row = _apart(gate, "gate", R, W)
     c, s = _f8_rows(codes, scales, R, W, dev)
     _launch("gdr_rms_norm", dev, stream, _norm_dims(R, H, W // H), io, x.data_ptr(), row, res, r,
-            order, g, g_row, w, float(eps), _opt(y, "y", (R, W), x.dtype, dev), c, s)
+            order, g, g_row, w, eps, _opt(y, "y", (R, W), dtype, dev), c, s)
 
 
 def gdr_quant_rows(x, codes, scales, *, stream=None):
     """Rows x [R,K] (float32 or bfloat16; they may lie apart) to codes [R,K]
     (float8_e4m3fn or uint8) and scales [R,ceil(K/128)] fp32."""
-    R, W, io, dev, row = _rows(x, "x")
+    (R, W), io, dev = _lead(x, "x", 2)
     if codes is None:
         raise ValueError("codes is required")
     c, s = _f8_rows(codes, scales, R, W, dev)
     # Any width: rows of whole blocks are heads of 128 channels side by side.
     H = W // 128 if W % 128 == 0 and W else 1
-    _launch("gdr_quant_rows", dev, stream, _norm_dims(R, H, W // H), io, x.data_ptr(), row, c, s)
+    _launch("gdr_quant_rows", dev, stream, _norm_dims(R, H, W // H), io, x.data_ptr(),
+            _apart(x, "x", R, W), c, s)
 
 
 def gdr_matmul_fp8(x, x_scales, w, w_scales, y, *, bias=None, stream=None):
