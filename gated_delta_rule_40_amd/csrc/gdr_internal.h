@@ -155,6 +155,7 @@ struct NormArgs {
   int res_bf16;         // dtype of the residual
   int gate_first;       // the gate goes before the norm
   int norm;             // 0: rows as they are
+  int through;          // how outputs are stored (set by the launch)
   float eps;
 };
 constexpr int kNormMaxD = 32768;
@@ -187,6 +188,7 @@ struct RopeArgs {
   long long x_stride;
   int B, T, H_q, H_kv, D, R;
   int interleaved;
+  int through;         // how outputs are stored (set by the launch)
   float magnitude;
 };
 hipError_t launch_rope(const RopeArgs& a, int io_bf16, hipStream_t stream);

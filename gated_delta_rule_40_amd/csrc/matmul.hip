@@ -22,6 +22,7 @@
 #include "device_common.hpp"
 #include "gdr.h"
 #include "gdr_internal.h"
+#include "store_through.hpp"
 
 namespace gdr {
 namespace {
@@ -82,22 +83,23 @@ __device__ __forceinline__ i32x8 join(i32x4 lo, i32x4 hi) {
 
 // 16 bytes a lane from `base` (the same in every lane) + offset to LDS: lane l's go
 // to lds + 16 l.  Nothing waits for it here.  (m0, which takes the address in LDS, is
-// set by the compiler right before what needs it.)
+// set by the compiler right before what needs it.  The wait states: one behind the write
+// of m0, five behind a vector instruction's of a scalar base.)
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, unsigned offset, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(lds), "v"(offset), "s"(base)
                : "memory");
 }
 __device__ __forceinline__ void load_to_lds(const uint8_t* p, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(lds), "v"(p)
                : "memory");
 }
 // 4 bytes a lane, lane l's to lds + 4 l.
 __device__ __forceinline__ void load_word_to_lds(const float* p, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, off"
                :
                : "s"(lds), "v"(p)
                : "memory");
@@ -131,9 +133,7 @@ __device__ __forceinline__ void store_out(const MatmulArgs& a, int m, int n, f32
 }
 
 // Eight neighbouring outputs of row m from column n; `whole`: the columns are there, and
-// 16-byte aligned.  Plain stores: past the caches they are faster alone (4000 x 8192 x
-// 4096 156 against 168 us), but what reads the outputs next then takes longer (with the
-// convolution behind it 194 against 191 us, with plain 8-bit rows 187 against 183).
+// 16-byte aligned.
 template <typename T>
 __device__ __forceinline__ void store_out8(const MatmulArgs& a, int m, int n, f32x4 lo, f32x4 hi,
                                            bool whole) {
@@ -154,8 +154,12 @@ __device__ __forceinline__ void store_out8(const MatmulArgs& a, int m, int n, f3
       e[4 + u] = from_f32<T>(hi[u]);
     }
 #pragma unroll
-    for (int c = 0; c < static_cast<int>(sizeof(T)) / 2; ++c)
-      reinterpret_cast<uint4*>(y)[c] = reinterpret_cast<const uint4*>(e)[c];
+    for (int c = 0; c < static_cast<int>(sizeof(T)) / 2; ++c) {
+      if constexpr (sizeof(T) == 2)
+        store_through(y, reinterpret_cast<const through_u32x4*>(e)[c]);
+      else  // two stores, each of half the bytes of a line: through 310 against 284 us
+        reinterpret_cast<through_u32x4*>(y)[c] = reinterpret_cast<const through_u32x4*>(e)[c];
+    }
   } else {
 #pragma unroll
     for (int u = 0; u < 8; ++u)

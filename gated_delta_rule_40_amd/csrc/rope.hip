@@ -13,6 +13,7 @@
 #include "device_common.hpp"
 #include "gdr.h"
 #include "gdr_internal.h"
+#include "store_through.hpp"
 
 namespace gdr {
 namespace {
@@ -56,11 +57,14 @@ __device__ __forceinline__ Piece<T, VEC> load_piece(const T* p) {
 }
 
 template <typename T, int VEC>
-__device__ __forceinline__ void store_piece(T* p, const Piece<T, VEC>& r) {
+__device__ __forceinline__ void store_piece(T* p, const Piece<T, VEC>& r, int through) {
   if constexpr (VEC * sizeof(T) == 16) {
-    uint4 w;
+    through_u32x4 w;
     __builtin_memcpy(&w, &r, 16);
-    *reinterpret_cast<uint4*>(p) = w;
+    if (through)
+      store_through(p, w);
+    else
+      *reinterpret_cast<through_u32x4*>(p) = w;
   } else {
 #pragma unroll
     for (int u = 0; u < VEC; ++u) p[u] = r.e[u];
@@ -161,10 +165,10 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a, int tokens, 
           v.e[e] = from_f32<T>(turn_first(p, q, w));
           z.e[e] = from_f32<T>(turn_second(p, q, w));
         }
-        store_piece<T, VEC>(to + half, z);
+        store_piece<T, VEC>(to + half, z, a.through);
       }
     }
-    store_piece<T, VEC>(to, v);
+    store_piece<T, VEC>(to, v, a.through);
   }
 }
 
@@ -200,7 +204,13 @@ hipError_t launch_io(const RopeArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_rope(const RopeArgs& a, int io_bf16, hipStream_t stream) {
+hipError_t launch_rope(const RopeArgs& args, int io_bf16, hipStream_t stream) {
+  RopeArgs a = args;
+  // Outputs that would fill the L2 caches go through them: 4000 tokens of 48 heads of 128
+  // 19.5 against 18.3 us, 500 5.1 against 5.2, 64 3.9 against 4.5.
+  const long long out = static_cast<long long>(a.B) * a.T * (a.H_q + (a.v ? 2 : 1) * a.H_kv) *
+                        a.D * (io_bf16 ? 2 : 4);
+  a.through = out >= (16 << 20);
   return io_bf16 ? launch_io<bf16>(a, stream) : launch_io<float>(a, stream);
 }
 
