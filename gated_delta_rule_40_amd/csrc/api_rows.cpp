@@ -21,13 +21,18 @@ int check_norm_sizes(const gdr_norm_dims* d, gdr_dtype io, int64_t x_stride) {
   if (!d) return GDR_E_NULL;
   if (!known_io(io)) return GDR_E_DTYPE;
   if (d->R < 0 || d->H <= 0 || d->D <= 0) return GDR_E_SHAPE;
-  if (!within(INT32_MAX, {d->H, d->D})) return GDR_E_SHAPE;
+  // A row's channels, and those a workgroup's threads reach past its end, are 32-bit.
+  if (!within(INT32_MAX - 2 * gdr::kNormMaxD, {d->H, d->D})) return GDR_E_SHAPE;
   if (x_stride < static_cast<int64_t>(d->H) * d->D) return GDR_E_SHAPE;
   if (d->D > gdr::kNormMaxD) return GDR_E_UNSUPPORTED;
   if (d->H > 1 && d->D % 128 != 0 && d->D != 16 && d->D != 32 && d->D != 64)
     return GDR_E_UNSUPPORTED;
-  // At most one workgroup per head, or per 512 channels of short heads.
-  if (!within(gdr::kMaxGrid, {d->R, d->H})) return GDR_E_SHAPE;
+  // Short heads: 32-bit numbers of vectors of 8 channels, rows padded to whole blocks;
+  // others: a workgroup a head.
+  const long long slots = (static_cast<long long>(d->H) * d->D + 127) / 128 * 16;
+  if (gdr::norm_short_head(d->D) ? !within(UINT32_MAX - 512ll, {d->R, slots})
+                                 : !within(gdr::kMaxGrid, {d->R, d->H}))
+    return GDR_E_SHAPE;
   if (!within(INT64_MAX / 16, {d->R, x_stride})) return GDR_E_SHAPE;
   return GDR_OK;
 }

@@ -159,6 +159,10 @@ struct NormArgs {
   float eps;
 };
 constexpr int kNormMaxD = 32768;
+// Heads that lie within a wave.
+inline bool norm_short_head(int D) {
+  return D == 16 || D == 32 || D == 64 || D == 128 || D == 256 || D == 512;
+}
 hipError_t launch_norm(const NormArgs& a, int io_bf16, hipStream_t stream);
 
 // Argument block of the 8-bit product.

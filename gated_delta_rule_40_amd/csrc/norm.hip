@@ -254,7 +254,7 @@ struct Vectors {
 template <typename T, bool ALIGNED, int LANES>
 __global__ __launch_bounds__(256) void head_kernel(NormArgs a, unsigned slots, double inverse_n) {
   const int W = a.H * a.D;
-  const unsigned idx = blockIdx.x * 256u + threadIdx.x;  // within 2^30
+  const unsigned idx = blockIdx.x * 256u + threadIdx.x;
   Vectors<T, ALIGNED, 1> v;
   v.row[0] = idx / slots;
   v.col[0] = idx % slots * 8;

@@ -178,6 +178,28 @@ def test_what_is_not_finite_stays_in_its_row(W):
                     torch.zeros(6, W, dtype=ref.F64))
 
 
+@pytest.mark.parametrize("R,H,D", [(1_200_000, 16, 16), (560_000, 1, 4096), (700_000, 8, 512)])
+def test_many_rows(R, H, D):
+    """More heads than workgroups, and tensors of more than 2^31 values."""
+    require_gpu()
+    announce(f"norm of many rows R={R} H={H} D={D}")
+    W = H * D
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    rows = torch.tensor([0, 1, R // 2, R - 2, R - 1], device=DEV)
+    x = torch.zeros(R, W, dtype=torch.bfloat16, device=DEV)
+    x[rows] = torch.randn(len(rows), W, generator=gen, device=DEV).bfloat16()
+    w = torch.rand(H, D, generator=gen, device=DEV)
+    y = torch.empty_like(x)
+    codes = torch.empty(R, W, dtype=F8, device=DEV)
+    scales = torch.empty(R, W // 128, device=DEV)
+    gdr.gdr_rms_norm(x, w, y, codes, scales)
+    want, _, units = ref.norm(x[rows].cpu(), w.cpu(), 1e-6, heads=H)
+    check([t.view(torch.uint8)[rows].view(F8) if t.dtype == F8 else t[rows]
+           for t in (y, codes, scales)], want, units, torch.bfloat16)
+    y[rows] = 0
+    assert not y.any() and (scales.min() == 2.0 ** -100).all()
+
+
 def test_no_rows():
     require_gpu()
     announce("norm and quant of no rows")

@@ -101,6 +101,25 @@ def test_steps_equal_a_prompt(Hq, Hkv):
                            whole[:, t:t + 1])
 
 
+def test_many_tokens():
+    """Rows of more than 2^31 values."""
+    require_gpu()
+    announce("rope of 540000 tokens")
+    T, D = 540_000, 128
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    rows = torch.tensor([0, 7, T // 2, T - 1], device=DEV)
+    x = torch.zeros(1, T, 32 * D, dtype=torch.bfloat16, device=DEV)
+    x[0, rows] = torch.randn(len(rows), 32 * D, generator=gen, device=DEV).bfloat16()
+    pos = torch.tensor([5], dtype=torch.int32)
+    got = run(x, freqs(D), pos, 24, 4, D, False)
+    for r in rows.tolist():
+        want, mag = ref.rope(x[:, r:r + 1].cpu(), freqs(D), pos + r, 24, 4, D, False, 1.0)
+        assert layer_ref.worst(got[:, r:r + 1].cpu(), want,
+                               ref.rope_bound(want, mag, x.dtype, 5 + r) + 1e-37) <= 1
+    got[0, rows] = 0
+    assert not got.any()
+
+
 def test_what_is_not_finite_stays_in_its_pair():
     require_gpu()
     announce("rope with inf and NaN")

@@ -35,7 +35,9 @@ def norm(R=3, H=2, D=128, io=1, x=A[0], stride=None, res=1, residual=None, order
     (dict(order=-1), "DTYPE"), (dict(res=2, residual=A[6]), "DTYPE"),
     (dict(R=-1), "SHAPE"), (dict(H=0), "SHAPE"), (dict(D=0), "SHAPE"), (dict(D=-128), "SHAPE"),
     (dict(H=2 ** 24, D=128), "SHAPE"), (dict(stride=255), "SHAPE"), (dict(stride=-256), "SHAPE"),
-    (dict(R=2 ** 24), "SHAPE"), (dict(R=2 ** 20, stride=2 ** 50), "SHAPE"),
+    (dict(R=2 ** 27), "SHAPE"), (dict(R=2 ** 24, H=1, D=4096), "SHAPE"),
+    (dict(R=2 ** 22, H=4, D=384), "SHAPE"), (dict(H=2 ** 24 - 1, D=128), "SHAPE"),
+    (dict(R=2 ** 20, stride=2 ** 50), "SHAPE"),
     (dict(order=1, gstride=255), "SHAPE"), (dict(order=2, R=2 ** 20, gstride=2 ** 50), "SHAPE"),
     (dict(H=1, D=32769), "UNSUPPORTED"), (dict(D=48), "UNSUPPORTED"), (dict(D=8), "UNSUPPORTED"),
     (dict(D=200), "UNSUPPORTED"),
