@@ -17,6 +17,10 @@
 //
 // Squares are summed in 64 bits: they cannot overflow, and rsqrt(mean + eps) = m 2^e
 // is applied as h 2^e m, so rows of any finite magnitude keep their digits.
+//
+// 4000 x 4096 bf16 with a residual to 8 bits 20.7 us (115 MB, 5.6 TB/s), one row 3.2 us,
+// 4000 x 8 heads x 512 gated 19.3 us, 4000 x 32 x 128 gated to 8 bits 20.0 us, plain rows
+// 4000 x 4096 to 8 bits 11.7 us, 777 x 2501 fp32 9.0 us.
 #include "device_common.hpp"
 #include "gdr.h"
 #include "gdr_internal.h"
@@ -343,8 +347,9 @@ hipError_t launch_sizes(const NormArgs& a, hipStream_t stream) {
     case 512: return launch_heads<T, ALIGNED, 64>(a, stream);
     default: break;
   }
-  // One vector a thread for few rows, two to four where rows fill the GPU.
-  const bool few = static_cast<long long>(a.R) * a.H < 1024;
+  // One vector a thread for few rows, two to four where rows fill the GPU (300 x 8192 7.6
+  // against 7.9 us, 1000 x 8192 15.5 against 13.9).
+  const bool few = static_cast<long long>(a.R) * a.H < 512;
   if (a.D <= 512) return launch_rows<T, ALIGNED, 64, 1>(a, stream);
   if (a.D <= 2048) return launch_rows<T, ALIGNED, 256, 1>(a, stream);
   if (a.D <= 4096)

@@ -10,6 +10,9 @@
 // are turned), the first ones loaded before the angles are formed.  (Two or four under
 // way together are slower: 20.0 and 20.8 against 18.5 us for 4000 tokens of 48 heads of
 // 128 in bf16.)  Bound by HBM, and by a launch and two chained loads for single tokens.
+//
+// 4000 tokens of 48 heads of 128 in bf16 18.3 us (98 MB, 5.4 TB/s), four ragged prompts
+// of up to 2047 tokens with half of each head turned 13.3 us, 64 single tokens 3.4 us.
 #include "device_common.hpp"
 #include "gdr.h"
 #include "gdr_internal.h"
