@@ -284,6 +284,7 @@ def test_calls_on_other_streams_at_once():
     for (go, outs), kept in zip(jobs, together):
         for t in outs:
             t.view(torch.uint8).zero_() if t.dtype == F8 else t.zero_()
+        torch.cuda.synchronize()  # the clearing is on this stream, the calls on theirs
         go()
         torch.cuda.synchronize()
         for a, b in zip(outs, kept):
