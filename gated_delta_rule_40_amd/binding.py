@@ -139,6 +139,10 @@ def load_library(path: Path | str | None = None):
     lib.gdr_strerror.restype = ctypes.c_char_p
     if path is None:
         _lib = lib
+        if _native is not None:
+            _native.bind(*(ctypes.cast(getattr(lib, n), vp).value for n in
+                           ("gdr_rms_norm", "gdr_quant_rows", "gdr_matmul_fp8", "gdr_rope")),
+                         _device, _raw_stream)
     return lib
 
 
@@ -312,9 +316,11 @@ except ImportError as _why:
         raise RuntimeError(f"_marshal.so cannot be loaded ({_unloaded}): build it with "
                            "`python -m gated_delta_rule_40_amd.build`") from _unloaded
     _opt = _ptr
+    _native = None
 else:
     _marshal.on_refusal(_refuse)
     _ptr, _opt = _marshal.ptr, _marshal.opt
+    _native = _marshal
 
 
 def _lead(t, name, dims):
@@ -348,6 +354,17 @@ def _launch(name, dev, stream, *args):
             rc = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != GDR_OK:
         raise GdrError(rc, name)
+
+
+def _whole(name):
+    """The native form of a whole call: its status, or None where the call is not a
+    plain one (then the Python path below takes or refuses it)."""
+    native = getattr(_native, name, None)
+    return native if native is not None else lambda *_: None
+
+
+_norm_call, _quant_call, _matmul_call, _rope_call = map(
+    _whole, ("rms_norm", "quant_rows", "matmul_fp8", "rope"))
 
 
 def _taps(weight):
@@ -544,6 +561,12 @@ def gdr_rms_norm(x, weight=None, y=None, codes=None, scales=None, *, residual=No
     multiplies the result, or x with gate_first).  Outputs: y [R,H*D] in x's dtype,
     codes [R,H*D] (float8_e4m3fn or uint8) with scales [R,ceil(H*D/128)] fp32, or
     both."""
+    if stream is None:
+        rc = _norm_call(x, weight, y, codes, scales, residual, gate, gate_first, heads, eps)
+        if rc is not None:
+            if rc:
+                raise GdrError(rc, "gdr_rms_norm")
+            return
     (R, W), io, dev = _lead(x, "x", 2)
     row, dtype, H, w = _apart(x, "x", R, W), x.dtype, heads, None
     if weight is not None:
@@ -577,6 +600,12 @@ def gdr_rms_norm(x, weight=None, y=None, codes=None, scales=None, *, residual=No
 def gdr_quant_rows(x, codes, scales, *, stream=None):
     """Rows x [R,K] (float32 or bfloat16; they may lie apart) to codes [R,K]
     (float8_e4m3fn or uint8) and scales [R,ceil(K/128)] fp32."""
+    if stream is None:
+        rc = _quant_call(x, codes, scales)
+        if rc is not None:
+            if rc:
+                raise GdrError(rc, "gdr_quant_rows")
+            return
     (R, W), io, dev = _lead(x, "x", 2)
     if codes is None:
         raise ValueError("codes is required")
@@ -591,6 +620,12 @@ def gdr_matmul_fp8(x, x_scales, w, w_scales, y, *, bias=None, stream=None):
     """Product of 8-bit rows x [M,K] (x_scales [M,ceil(K/128)] fp32) with an 8-bit
     weight w [N,K] (w_scales [ceil(N/128),ceil(K/128)] fp32), codes float8_e4m3fn or
     uint8: y [M,N] (float32 or bfloat16), bias [N] fp32 or None."""
+    if stream is None:
+        rc = _matmul_call(x, x_scales, w, w_scales, y, bias)
+        if rc is not None:
+            if rc:
+                raise GdrError(rc, "gdr_matmul_fp8")
+            return
     (M, N), io, dev = _lead(y, "y", 2)
     for name, t in (("x", x), ("w", w)):
         if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in _F8:
@@ -612,6 +647,12 @@ def gdr_rope(x, freq, pos, q, k, v=None, *, interleaved=False, magnitude=1.0, le
     freq [R/2] float64 radians a position (gdr_rope_freqs), pos [B] int32 the
     position of each row's first token, lens [B] int32 or None.  Without v the rows
     hold q and k alone."""
+    if stream is None:
+        rc = _rope_call(x, freq, pos, q, k, v, interleaved, magnitude, lens)
+        if rc is not None:
+            if rc:
+                raise GdrError(rc, "gdr_rope")
+            return
     (B, T, C), io, dev = _lead(x, "x", 3)
     for name, t in (("q", q), ("k", k)):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
