@@ -28,10 +28,12 @@ int check_norm_sizes(const gdr_norm_dims* d, gdr_dtype io, int64_t x_stride) {
   if (d->H > 1 && d->D % 128 != 0 && d->D != 16 && d->D != 32 && d->D != 64)
     return GDR_E_UNSUPPORTED;
   // Short heads: 32-bit numbers of vectors of 8 channels, rows padded to whole blocks;
-  // others: a workgroup a head.
+  // others: a workgroup a head, of 1024 threads past 8192 channels, else (where there are
+  // many) of up to 256.
   const long long slots = (static_cast<long long>(d->H) * d->D + 127) / 128 * 16;
   if (gdr::norm_short_head(d->D) ? !within(UINT32_MAX - 512ll, {d->R, slots})
-                                 : !within(gdr::kMaxGrid, {d->R, d->H}))
+                                 : !within(d->D > 8192 ? gdr::kMaxGrid / 4 : gdr::kMaxGrid,
+                                           {d->R, d->H}))
     return GDR_E_SHAPE;
   if (!within(INT64_MAX / 16, {d->R, x_stride})) return GDR_E_SHAPE;
   return GDR_OK;
@@ -68,7 +70,8 @@ int check_matmul_sizes(const gdr_matmul_dims* d, gdr_dtype io) {
   if (d->K % 16 != 0 || d->K > gdr::kMatmulMaxK) return GDR_E_UNSUPPORTED;
   // The ends of the last tiles are 32-bit.
   if (d->M > INT32_MAX - 256 || d->N > INT32_MAX - 256) return GDR_E_SHAPE;
-  if (gdr::matmul_grid(d->M, d->N, io == GDR_BF16) > gdr::kMaxGrid) return GDR_E_SHAPE;
+  // Workgroups of up to 1024 threads.
+  if (gdr::matmul_grid(d->M, d->N, io == GDR_BF16) > gdr::kMaxGrid / 4) return GDR_E_SHAPE;
   return GDR_OK;
 }
 

@@ -101,6 +101,17 @@ def test_matmul_refusals(case, expect):
     assert matmul(**case) == E[expect]
 
 
+@pytest.mark.parametrize("call,case", [
+    (norm, dict(R=2 ** 22, H=1, D=16384, stride=16384)),  # 1024 threads a row
+    (norm, dict(R=2 ** 22, H=1, D=16384, stride=16384, codes=None, scales=None)),
+    (quant, dict(R=2 ** 20, H=4, D=8320)),
+    (matmul, dict(m=1, n=2 ** 27, k=16)),                 # 512 threads for 16 outputs
+    (matmul, dict(m=16, n=2 ** 27, k=16, io=0)),
+])
+def test_launches_of_2_32_threads_are_refused(call, case):
+    assert call(**case) == E["SHAPE"]
+
+
 def rope(B=2, T=5, Hq=4, Hkv=2, D=64, R=64, io=1, pairs=0, x=A[0], stride=None, freq=A[1],
          pos=A[2], lens=None, q=A[3], k=A[4], v=A[5], dims=True):
     lib = gdr.load_library()
