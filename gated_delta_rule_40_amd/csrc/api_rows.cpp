@@ -70,8 +70,8 @@ int check_matmul_sizes(const gdr_matmul_dims* d, gdr_dtype io) {
   if (d->K % 16 != 0 || d->K > gdr::kMatmulMaxK) return GDR_E_UNSUPPORTED;
   // The ends of the last tiles are 32-bit.
   if (d->M > INT32_MAX - 256 || d->N > INT32_MAX - 256) return GDR_E_SHAPE;
-  // Workgroups of up to 1024 threads.
-  if (gdr::matmul_grid(d->M, d->N, io == GDR_BF16) > gdr::kMaxGrid / 4) return GDR_E_SHAPE;
+  // Workgroups of up to 512 threads (of 1024 only where there are few).
+  if (gdr::matmul_grid(d->M, d->N, d->K, io == GDR_BF16) > gdr::kMaxGrid / 2) return GDR_E_SHAPE;
   return GDR_OK;
 }
 

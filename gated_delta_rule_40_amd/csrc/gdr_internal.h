@@ -177,7 +177,7 @@ struct MatmulArgs {
 };
 constexpr int kMatmulMaxK = 1 << 20;
 // Workgroups launch_matmul starts for these sizes.
-long long matmul_grid(int M, int N, int io_bf16);
+long long matmul_grid(int M, int N, int K, int io_bf16);
 hipError_t launch_matmul(const MatmulArgs& a, int io_bf16, hipStream_t stream);
 
 // Argument block of the rotary positions.

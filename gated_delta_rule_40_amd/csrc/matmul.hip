@@ -17,14 +17,16 @@
 // stream_kernel: few rows.  The weight is read once; the blocks of a row are shared by
 // the waves of a workgroup and their sums joined in LDS.  Bound by HBM (one row through
 // 8192 x 4096 8.5 us, 34 MB), and with the rows by the L2 caches that every workgroup
-// reads x from (64 rows 11.5 us).
+// reads x from (64 rows 11.5 us; 64 x 1024 x 4096 5.8, K = 14336 12.0, in smaller tiles).
 // tile_kernel: many rows.  4000 rows through 8192 x 4096 133 us, 2.0 PFLOP/s; 8192^3 2.3.
 // The matrix pipes alone reach 3.5 on such codes, held by power (4.9 on zeros).  A step
 // of 2048 matrix cycles a SIMD takes about 3600: the loads into LDS cost some 400 of
 // the rest, reading operands 100, the barrier and what surrounds it most of it.
 // Tried without gain: two groups of waves half a block apart, a second barrier half way
-// with loads a block and a half ahead, the barrier before the last row of products,
+// with loads a block and a half ahead, the barrier before the last row of products (4%
+// faster here, 2 to 10% slower for K = 14336, 4080 and 500 rows),
 // the weight's operands two ahead, wave priorities.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -471,34 +473,58 @@ hipError_t launch_tile(const MatmulArgs& a, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// Which kernel.  Up to 16 and 32 rows a tile of as many; past that the one with the
-// lowest estimate, in microseconds for K = 4096, of a fixed cost and one for each
-// round of 256 workgroups (fitted to 20 sizes from 64 x 8192 to 4000 x 8192; it picked
-// the fastest or one within 5%).  Measured at its edges, each time against the next:
+// Which kernel.  Up to 16 rows a tile of as many; past that the one with the lowest
+// estimate, in microseconds, of a fixed cost and, for each round of 256 workgroups, one of
+// its own and one for 4096 channels of the rows that a workgroup loads (fitted to 504 sizes
+// from 20 x 512 to 1000 x 12288, K of 1024, 4096 and 14336, both output types: it takes
+// 0.6% longer than the fastest of them all on the average, at most 15%).  The tile_kernel is
+// left out up to 64 rows, where the weight is read once and HBM is what counts (17 x 65536
+// 57 us with 32 x 32, 70 with a tile of 64 x 128).  With few outputs smaller tiles reach
+// more CUs, each of which takes in some 68 bytes a ns:
+//   64 x 1024 stream 16 x 16 5.8 us, 32 x 16 5.6, 64 x 32 8.2; K = 14336 12.0, 12.6, 23.7
+//   128 x 1024 stream 16 x 16 8.3, 32 x 16 6.5, 32 x 32 7.2, 64 x 32 9.4
+//   64 x 4096 stream 32 x 16 9.5, 64 x 16 9.2, 64 x 32 10.1; K = 14336 25.7, 21.3, 24.8
+//   32 x 8192 stream 32 x 16 10.2, 32 x 32 10.0; 100 x 4096 64 x 16 14.4, 64 x 32 12.0
 //   64 x 8192 stream 64 x 32 12.2, stream 64 x 64 14.3; 64 x 16384 21.4, 16.7
 //   192 x 8192 stream 64 x 32 27.6, tile 64 x 128 24.6
 //   512 x 8192 tile 64 x 128 32.8, tile 128 x 128 31.8
 //   1000 x 8192 tile 128 x 128 49.1, tile 256 x 128 45.5
-//   1500 x 8192 tile 128 x 128 73.7, tile 256 x 256 62.6; 2500 x 8192 118.8, 125.3
+//   1500 x 8192 tile 128 x 128 73.7, tile 256 x 256 62.6
 // An fp32 output's operands take twice the registers: the two that would not fit are left
-// out, and the tiles' products take twice as long (1000 x 8192: 73.4 and 68.3).
+// out, and the tiles' products take longer (1000 x 8192: 73.4 and 68.3).
 // ---------------------------------------------------------------------------
-enum class Plan { kOne, kTwo, kStream32, kStream64, kTile64, kTile128, kTile256, kTile256x256 };
+enum class Plan {
+  kStream16x16,
+  kStream32x16,
+  kStream32x32,
+  kStream64x16,
+  kStream64x32,
+  kStream64x64,
+  kTile64,
+  kTile128,
+  kTile256,
+  kTile256x256
+};
 
 struct Option {
   Plan plan;
   int rows, cols;       // of a tile
-  float fixed, round;   // bf16 outputs
-  float fixed32, round32;
+  struct Cost {
+    float fixed, round, channels;
+  } bf16, fp32;  // by the type of the outputs
 };
 constexpr float kNever = 1e30f;
 constexpr Option kOptions[] = {
-    {Plan::kStream32, 64, 32, 5.0f, 7.2f, 5.0f, 7.2f},
-    {Plan::kStream64, 64, 64, 6.0f, 11.0f, 0.0f, kNever},
-    {Plan::kTile64, 64, 128, 10.0f, 12.0f, 14.0f, 16.5f},
-    {Plan::kTile128, 128, 128, 8.0f, 22.0f, 10.0f, 32.0f},
-    {Plan::kTile256, 256, 128, 2.0f, 43.0f, 0.0f, 68.0f},
-    {Plan::kTile256x256, 256, 256, 0.0f, 66.0f, 0.0f, kNever},
+    {Plan::kStream16x16, 16, 16, {0.0f, 1.5f, 2.4f}, {0.0f, 1.5f, 2.4f}},
+    {Plan::kStream32x16, 32, 16, {0.4f, 2.2f, 3.0f}, {0.4f, 2.2f, 3.0f}},
+    {Plan::kStream32x32, 32, 32, {2.2f, 1.3f, 4.1f}, {2.2f, 1.3f, 4.1f}},
+    {Plan::kStream64x16, 64, 16, {1.2f, 2.1f, 5.3f}, {1.2f, 2.1f, 5.3f}},
+    {Plan::kStream64x32, 64, 32, {1.6f, 3.0f, 6.2f}, {1.6f, 3.0f, 6.2f}},
+    {Plan::kStream64x64, 64, 64, {0.0f, 6.3f, 7.2f}, {kNever, 0.0f, 0.0f}},
+    {Plan::kTile64, 64, 128, {3.5f, 1.1f, 19.1f}, {4.5f, 0.0f, 28.8f}},
+    {Plan::kTile128, 128, 128, {10.7f, 1.6f, 20.9f}, {11.7f, 1.0f, 35.1f}},
+    {Plan::kTile256, 256, 128, {6.5f, 8.2f, 33.3f}, {0.0f, 14.1f, 56.5f}},
+    {Plan::kTile256x256, 256, 256, {5.9f, 9.4f, 50.4f}, {kNever, 0.0f, 0.0f}},
 };
 
 struct Choice {
@@ -508,14 +534,16 @@ struct Choice {
 long long tiles_of(int M, int N, int rows, int cols) {
   return ((M + rows - 1ll) / rows) * ((N + cols - 1ll) / cols);
 }
-Choice choose(int M, int N, bool fp32) {
-  if (M <= 16) return Choice{Plan::kOne, tiles_of(M, N, 16, 16)};
-  if (M <= 32) return Choice{Plan::kTwo, tiles_of(M, N, 32, 32)};
+Choice choose(int M, int N, int K, bool fp32) {
+  if (M <= 16) return Choice{Plan::kStream16x16, tiles_of(M, N, 16, 16)};
   Choice best = {};
   float least = 0.0f;
   for (const Option& o : kOptions) {
     const long long tiles = tiles_of(M, N, o.rows, o.cols), rounds = (tiles + 255) / 256;
-    const float cost = (fp32 ? o.fixed32 : o.fixed) + (fp32 ? o.round32 : o.round) * rounds;
+    const Option::Cost& c = fp32 ? o.fp32 : o.bf16;
+    const float loaded = static_cast<float>(std::min(M, o.rows) + o.cols) / (o.rows + o.cols);
+    const float cost = c.fixed + (c.round + c.channels * loaded * (K / 4096.0f)) * rounds;
+    if (M <= 64 && o.plan >= Plan::kTile64) break;
     if (best.tiles == 0 || cost < least) {
       best = Choice{o.plan, tiles};
       least = cost;
@@ -524,20 +552,35 @@ Choice choose(int M, int N, bool fp32) {
   return best;
 }
 
+// Whether 16 x 16 tiles take 16 waves, not 8.  With a workgroup a CU and up to 8 rows a CU
+// waits for the weight's loads, of which more waves have more under way (1 x 2560, K =
+// 14336 8.6 against 10.9 us); 16 rows gain nothing (16 x 4096, K = 14336 12.8 and 12.0), nor
+// do waves without a block of their own (1 x 12288, K = 1024 6.4 and 4.9).  Two workgroups
+// fit a CU: past one each they have to fill the CUs evenly and, with one block a wave after
+// another, not take too long (1 x 8192, K = 4096 8.7 and 9.1, 16 x 8192 9.4 and 9.8, but 1 x
+// 5120 7.4 and 7.0; K = 14336 16.3 and 13.6).
+bool wide(const MatmulArgs& a, long long tiles) {
+  const int blocks = (a.K + kBlock - 1) / kBlock;
+  if (a.M > 16 || blocks < 16) return false;
+  if (tiles <= 256) return a.M <= 8;
+  return blocks <= 64 && tiles * 8 >= (tiles + 511) / 512 * 512 * 7;
+}
+
 template <typename T>
 hipError_t launch_io(const MatmulArgs& a, hipStream_t stream) {
-  switch (choose(a.M, a.N, sizeof(T) == 4).plan) {
-    case Plan::kOne:
-      // One block or two a wave: 1 x 8192, K = 4096 8.6 against 9.1 us with 8 waves; 16 x
-      // 4096, K = 14336 12.3 against 11.4.
-      return a.K <= 64 * kBlock ? launch_stream<T, 1, 1, 16>(a, stream)
-                                : launch_stream<T, 1, 1, 8>(a, stream);
-    case Plan::kTwo: return launch_stream<T, 2, 2, 8>(a, stream);
-    case Plan::kStream32: return launch_stream<T, 4, 2, 8>(a, stream);
+  const Choice choice = choose(a.M, a.N, a.K, sizeof(T) == 4);
+  switch (choice.plan) {
+    case Plan::kStream16x16:
+      return wide(a, choice.tiles) ? launch_stream<T, 1, 1, 16>(a, stream)
+                                   : launch_stream<T, 1, 1, 8>(a, stream);
+    case Plan::kStream32x16: return launch_stream<T, 2, 1, 8>(a, stream);
+    case Plan::kStream32x32: return launch_stream<T, 2, 2, 8>(a, stream);
+    case Plan::kStream64x16: return launch_stream<T, 4, 1, 8>(a, stream);
+    case Plan::kStream64x32: return launch_stream<T, 4, 2, 8>(a, stream);
     case Plan::kTile64: return launch_tile<T, 2, 2, 4, 2>(a, stream);
     case Plan::kTile128: return launch_tile<T, 2, 2, 4, 4>(a, stream);
     case Plan::kTile256: return launch_tile<T, 2, 4, 4, 4>(a, stream);
-    case Plan::kStream64:
+    case Plan::kStream64x64:
       if constexpr (sizeof(T) == 2) return launch_stream<T, 4, 4, 8>(a, stream);
       break;
     case Plan::kTile256x256:
@@ -549,7 +592,9 @@ hipError_t launch_io(const MatmulArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-long long matmul_grid(int M, int N, int io_bf16) { return choose(M, N, !io_bf16).tiles; }
+long long matmul_grid(int M, int N, int K, int io_bf16) {
+  return choose(M, N, K, !io_bf16).tiles;
+}
 
 hipError_t launch_matmul(const MatmulArgs& a, int io_bf16, hipStream_t stream) {
   return io_bf16 ? launch_io<bf16>(a, stream) : launch_io<float>(a, stream);

@@ -79,6 +79,20 @@ def test_every_tiling(M, N, K, io):
     check(inputs(M + N, M, N, K), io_dtype(io))
 
 
+# The tilings of few rows, or of few outputs for the rows there are; blocks enough that
+# each of their waves takes several.
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(7, 300, 2064), (8, 1003, 4112), (8, 8192, 2048), (9, 300, 4112),
+                                   (20, 1000, 1040), (45, 2001, 2064), (48, 4096, 1296),
+                                   (33, 4100, 2064), (64, 4099, 1040), (100, 2003, 4112),
+                                   (200, 1003, 4000), (250, 4001, 1040), (60, 16003, 1296),
+                                   (500, 8100, 2064), (990, 8190, 1040), (1500, 8001, 2064)])
+def test_tilings_of_few_rows_or_outputs(M, N, K, io):
+    require_gpu()
+    announce(f"matmul tiling of few M={M} N={N} K={K} io={io}")
+    check(inputs(M + N, M, N, K), io_dtype(io))
+
+
 @pytest.mark.parametrize("M,N,K", [(4000, 8192, 4096), (2047, 4100, 1040), (1, 8192, 14336),
                                    (64, 4096, 14336), (4097, 128, 4096), (5000, 16, 256),
                                    (16, 20000, 512)])
