@@ -16,8 +16,8 @@
 //
 // stream_kernel: few rows.  The weight is read once; the blocks of a row are shared by
 // the waves of a workgroup and their sums joined in LDS.  Bound by HBM (one row through
-// 8192 x 4096 8.5 us, 34 MB), and with the rows by the L2 caches that every workgroup
-// reads x from (64 rows 11.5 us; 64 x 1024 x 4096 5.8, K = 14336 12.0, in smaller tiles).
+// 8192 x 4096 7.9 us, 34 MB), and with the rows by the L2 caches that every workgroup
+// reads x from (64 rows 11.0 us; 64 x 1024 x 4096 5.8, K = 14336 12.0, in smaller tiles).
 // tile_kernel: many rows.  4000 rows through 8192 x 4096 133 us, 2.0 PFLOP/s; 8192^3 2.3.
 // The matrix pipes alone reach 3.5 on such codes, held by power (4.9 on zeros).  A step
 // of 2048 matrix cycles a SIMD takes about 3600: the loads into LDS cost some 400 of
@@ -230,11 +230,19 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(MatmulArgs a, int ro
     }
     load_word_to_lds(sx + b, lds + kRows * kBlock);
   };
-  if (wave < blocks) fetch(wave);
+  // Rows a multiple of 4 KiB apart lie on the same memory channels: workgroups (32 at a time,
+  // four of each XCD, which may share a weight's or x's rows) then begin at different blocks.
+  // 64 x 4096 x 4096 10.2 -> 8.5 us, 64 x 8192 12.1 -> 11.1, 1 x 8192 8.6 -> 7.8; other
+  // strides gain nothing (16 x 4096, K = 14336 11.5 and 12.1).
+  const unsigned turn = K % 4096 == 0 ? blockIdx.x / 32 * WAVES : 0;
+  const int first = blocks > 0 ? static_cast<int>(turn % blocks) : 0;
+  auto block_of = [&](int t) { return t + first < blocks ? t + first : t + first - blocks; };
+  if (wave < blocks) fetch(block_of(wave));
 
   f32x4 acc[NT][MT] = {};
   const int p0 = (g ^ (in % 8)) * 16, p1 = p0 ^ 64;
-  for (int b = wave; b < blocks; b += WAVES) {
+  for (int t = wave; t < blocks; t += WAVES) {
+    const int b = block_of(t);
     wait_loads();
     auto operand = [&](int row) {
       const uint8_t* p = place + (row + in) * kBlock;
@@ -252,7 +260,7 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(MatmulArgs a, int ro
       s[j] = *reinterpret_cast<const float*>(place + kRows * kBlock + (16 * j + in) * 4) * sw[b];
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // all read: the place is free
-    if (b + WAVES < blocks) fetch(b + WAVES);
+    if (t + WAVES < blocks) fetch(block_of(t + WAVES));
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -475,9 +483,9 @@ hipError_t launch_tile(const MatmulArgs& a, hipStream_t stream) {
 // ---------------------------------------------------------------------------
 // Which kernel.  Up to 16 rows a tile of as many; past that the one with the lowest
 // estimate, in microseconds, of a fixed cost and, for each round of 256 workgroups, one of
-// its own and one for 4096 channels of the rows that a workgroup loads (fitted to 504 sizes
-// from 20 x 512 to 1000 x 12288, K of 1024, 4096 and 14336, both output types: it takes
-// 0.6% longer than the fastest of them all on the average, at most 15%).  The tile_kernel is
+// its own and one for 4096 channels of the rows that a workgroup loads (680 sizes from 20 x
+// 512 to 1000 x 12288, K of 1024 to 14336, both output types: it takes 0.7% longer than the
+// fastest of them all on the average, more than 10% at 2% of them).  The tile_kernel is
 // left out up to 64 rows, where the weight is read once and HBM is what counts (17 x 65536
 // 57 us with 32 x 32, 70 with a tile of 64 x 128).  With few outputs smaller tiles reach
 // more CUs, each of which takes in some 68 bytes a ns:

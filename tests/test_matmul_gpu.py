@@ -93,6 +93,17 @@ def test_tilings_of_few_rows_or_outputs(M, N, K, io):
     check(inputs(M + N, M, N, K), io_dtype(io))
 
 
+# Rows a multiple of 4 KiB apart, whose workgroups begin at different blocks.
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 8192, 4096), (5, 6000, 8192), (16, 1600, 4096),
+                                   (30, 5003, 4096), (40, 4100, 12288), (64, 8192, 4096),
+                                   (61, 16003, 4096), (130, 2001, 8192), (250, 1000, 4096)])
+def test_rows_of_whole_pages(M, N, K, io):
+    require_gpu()
+    announce(f"matmul rows of whole pages M={M} N={N} K={K} io={io}")
+    check(inputs(M + N, M, N, K), io_dtype(io))
+
+
 @pytest.mark.parametrize("M,N,K", [(4000, 8192, 4096), (2047, 4100, 1040), (1, 8192, 14336),
                                    (64, 4096, 14336), (4097, 128, 4096), (5000, 16, 256),
                                    (16, 20000, 512)])
