@@ -18,7 +18,7 @@
 // the waves of a workgroup and their sums joined in LDS.  Bound by HBM (one row through
 // 8192 x 4096 7.9 us, 34 MB), and with the rows by the L2 caches that every workgroup
 // reads x from (64 rows 11.0 us; 64 x 1024 x 4096 5.8, K = 14336 12.0, in smaller tiles).
-// tile_kernel: many rows.  4000 rows through 8192 x 4096 133 us, 2.0 PFLOP/s; 8192^3 2.3.
+// tile_kernel: many rows.  4000 rows through 8192 x 4096 129 us, 2.1 PFLOP/s; 8192^3 2.3.
 // The matrix pipes alone reach 3.5 on such codes, held by power (4.9 on zeros).  A step
 // of 2048 matrix cycles a SIMD takes about 3600: the loads into LDS cost some 400 of
 // the rest, reading operands 100, the barrier and what surrounds it most of it.
@@ -389,19 +389,26 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(MatmulArgs a, int ro
   // one of 64.  (One load a row and block touched a line for 4 bytes: 157 us without
   // these loads against 192 with them.)
   float rs[MT], ws = 0.0f;
-  auto load_scales = [&](int b) {  // b a multiple of 4
+  auto load_scales = [&](int b, bool start) {  // b a multiple of 4; the first one?
 #pragma unroll
     for (int j = 0; j < MT; ++j) rs[j] = sx[j][min(b + g, blocks - 1)];
-    if (b % 64 == 0) ws = sw[min(b + lane, blocks - 1)];
+    if (start || b % 64 == 0) ws = sw[min(b / 64 * 64 + lane, blocks - 1)];
   };
+  // Every XCD (whose workgroups share what they load) begins at a block of its own, in whole
+  // groups of four blocks, so that the XCDs do not ask for the same channels of memory:
+  // 4000 x 8192 x 4096 134 -> 129 us, K = 8192 261 -> 250, K = 5120 158 -> 155, 1000 x 8192,
+  // K = 14336 163 -> 155; 4000 x 4096, K = 14336 205 -> 207.
+  const int first = K % 512 == 0 ? static_cast<int>(blockIdx.x % 8) * (blocks / 32 * 4) : 0;
+  auto block_of = [&](int t) { return t + first < blocks ? t + first : t + first - blocks; };
   if (blocks > 0) {
-    load_scales(0);
-    fetch_all(0);
+    load_scales(block_of(0), true);
+    fetch_all(block_of(0));
   }
   f32x4 acc[NT][MT] = {};
-  // One block; AHEAD: the next is there, and whole.
-  auto step = [&](int b, auto ahead) {
+  // One block, the t-th; AHEAD: the next is there, and whole.
+  auto step = [&](int t, auto ahead) {
     constexpr bool AHEAD = decltype(ahead)::value;
+    const int b = block_of(t), next = block_of(t + 1);
     wait_loads();
     __syncthreads();  // this block is in LDS, and no wave reads the one before
     const float wb = __builtin_bit_cast(
@@ -414,9 +421,9 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(MatmulArgs a, int ro
                                                 __builtin_bit_cast(int, rs[j])));
       asm volatile("" : "+v"(s[j]));  // here: a later use would wait for the loads below
     }
-    if (AHEAD || b + 1 < blocks) {
-      if (b % 4 == 3) load_scales(b + 1);
-      if (!AHEAD) fetch_all(b + 1);
+    if (AHEAD || t + 1 < blocks) {
+      if (b % 4 == 3) load_scales(next, false);
+      if (!AHEAD) fetch_all(next);
     }
 
     const uint8_t* lw = tile[b & 1] + (wn + in / 4 * 8 + in % 4) * kBlock;
@@ -446,7 +453,7 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(MatmulArgs a, int ro
         // The next block's loads, one behind each product: all at once they would hold
         // the wave up until the memory pipe has taken them (161 against 154 us), later
         // ones arrive late (156 to 163).
-        if (AHEAD && q < kEach) fetch(b + 1, q);
+        if (AHEAD && q < kEach) fetch(next, q);
       }
       if (q >= kLag) {
         const int p = q - kLag;
@@ -456,9 +463,9 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(MatmulArgs a, int ro
     }
   };
   const int whole = K / kBlock;
-  int b = 0;
-  for (; b + 1 < whole; ++b) step(b, std::true_type{});
-  for (; b < blocks; ++b) step(b, std::false_type{});
+  int t0 = 0;
+  for (; t0 + 1 < whole; ++t0) step(t0, std::true_type{});
+  for (; t0 < blocks; ++t0) step(t0, std::false_type{});
   // A lane holds 8 neighbouring outputs in a pair of products.
   const int m = m0 + wm + in, n = n0 + wn + 8 * g;
   const bool whole_row = n0 + BN <= a.N && a.N % (16 / static_cast<int>(sizeof(T))) == 0;

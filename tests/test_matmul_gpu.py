@@ -93,11 +93,13 @@ def test_tilings_of_few_rows_or_outputs(M, N, K, io):
     check(inputs(M + N, M, N, K), io_dtype(io))
 
 
-# Rows a multiple of 4 KiB apart, whose workgroups begin at different blocks.
+# Rows a multiple of 4 KiB or 512 bytes apart, whose workgroups begin at different blocks.
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(1, 8192, 4096), (5, 6000, 8192), (16, 1600, 4096),
                                    (30, 5003, 4096), (40, 4100, 12288), (64, 8192, 4096),
-                                   (61, 16003, 4096), (130, 2001, 8192), (250, 1000, 4096)])
+                                   (61, 16003, 4096), (130, 2001, 8192), (250, 1000, 4096),
+                                   (400, 5003, 4608), (1000, 8190, 8704), (1100, 8001, 4608),
+                                   (1500, 8001, 8704), (1536, 8192, 12288), (700, 8100, 17408)])
 def test_rows_of_whole_pages(M, N, K, io):
     require_gpu()
     announce(f"matmul rows of whole pages M={M} N={N} K={K} io={io}")
