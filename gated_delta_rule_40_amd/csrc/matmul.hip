@@ -16,7 +16,7 @@
 //
 // stream_kernel: few rows.  The weight is read once; the blocks of a row are shared by
 // the waves of a workgroup and their sums joined in LDS.  Bound by HBM (one row through
-// 8192 x 4096 7.9 us, 34 MB), and with the rows by the L2 caches that every workgroup
+// 8192 x 4096 7.8 us, 34 MB), and with the rows by the L2 caches that every workgroup
 // reads x from (64 rows 11.0 us; 64 x 1024 x 4096 5.8, K = 14336 12.0, in smaller tiles).
 // tile_kernel: many rows.  4000 rows through 8192 x 4096 129 us, 2.1 PFLOP/s; 8192^3 2.3.
 // The matrix pipes alone reach 3.5 on such codes, held by power (4.9 on zeros).  A step
@@ -569,16 +569,11 @@ Choice choose(int M, int N, int K, bool fp32) {
 
 // Whether 16 x 16 tiles take 16 waves, not 8.  With a workgroup a CU and up to 8 rows a CU
 // waits for the weight's loads, of which more waves have more under way (1 x 2560, K =
-// 14336 8.6 against 10.9 us); 16 rows gain nothing (16 x 4096, K = 14336 12.8 and 12.0), nor
-// do waves without a block of their own (1 x 12288, K = 1024 6.4 and 4.9).  Two workgroups
-// fit a CU: past one each they have to fill the CUs evenly and, with one block a wave after
-// another, not take too long (1 x 8192, K = 4096 8.7 and 9.1, 16 x 8192 9.4 and 9.8, but 1 x
-// 5120 7.4 and 7.0; K = 14336 16.3 and 13.6).
+// 14336 8.6 against 10.9 us).  16 rows gain nothing (16 x 4096, K = 14336 13.0 and 12.3), nor
+// do waves without a block of their own (1 x 4096, K = 1024 3.8 and 3.6) or more workgroups
+// (1 x 8192, K = 4096 8.1 and 7.9; 1 x 5120, K = 14336 16.3 and 13.5).
 bool wide(const MatmulArgs& a, long long tiles) {
-  const int blocks = (a.K + kBlock - 1) / kBlock;
-  if (a.M > 16 || blocks < 16) return false;
-  if (tiles <= 256) return a.M <= 8;
-  return blocks <= 64 && tiles * 8 >= (tiles + 511) / 512 * 512 * 7;
+  return a.M <= 8 && a.K >= 16 * kBlock && tiles <= 256;
 }
 
 template <typename T>
