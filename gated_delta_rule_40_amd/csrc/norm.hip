@@ -75,14 +75,15 @@ __device__ __forceinline__ float row16_max(float x) {
 
 // 1 / sqrt(ss / n + eps) = m * p, p a power of two (exact also where fp32 holds it
 // only as a subnormal).  The hardware's root is good to 2^-23; one step of Newton's
-// method doubles the digits.
+// method doubles the digits.  A sum that is infinite (as no finite h's is) has the root 0,
+// which the step would turn into NaN.
 struct Root {
   float m, p;
 };
 __device__ __forceinline__ Root inverse_root(double ss, double inverse_n, float eps) {
   const double v = ss * inverse_n + static_cast<double>(eps);
   double r = __builtin_amdgcn_rsq(v);
-  r = __builtin_fma(0.5 * r, __builtin_fma(-v * r, r, 1.0), r);
+  r = r == 0.0 ? 0.0 : __builtin_fma(0.5 * r, __builtin_fma(-v * r, r, 1.0), r);
   return Root{static_cast<float>(__builtin_amdgcn_frexp_mant(r)),
               ldexpf(1.0f, __builtin_amdgcn_frexp_exp(r))};
 }

@@ -482,8 +482,9 @@ typedef enum gdr_norm_gate {
  *             to the io dtype; both or neither NULL, and not NULL together with y
  *
  * residual, y, codes and scales must not overlap each other or an input.  Sums
- * of squares are 64-bit: rows of any finite fp32 magnitude have a finite norm
- * (an h past fp32's range is infinite).
+ * of squares are 64-bit: rows of any finite fp32 magnitude have a finite norm.
+ * An h past fp32's range is infinite; a head that holds an infinity is 0 at its
+ * finite channels and NaN at the infinite ones.
  */
 int gdr_rms_norm(const gdr_norm_dims* dims, gdr_dtype io, const void* x, int64_t x_stride,
                  gdr_dtype res, void* residual, gdr_norm_gate order, const void* gate,
