@@ -238,7 +238,7 @@ int gdr_prefill_chunked_noalloc(const gdr_dims* dims, gdr_dtype io, gdr_gate gat
  *
  * Numbers: states, sums and softmax statistics are fp32 or wider.  An output in
  * bf16 is rounded once, from a sum whose terms are within 2^-15 of themselves or
- * better.  What depends on an input that is not finite may be infinite or NaN
+ * better (gdr_matmul_fp8 states its own).  What depends on an input that is not finite may be infinite or NaN
  * (which of the two can differ between a function's forms); nothing else is.
  * ------------------------------------------------------------------------ */
 
@@ -440,7 +440,9 @@ int gdr_attn_cached(const gdr_kv_dims* dims, gdr_dtype io, const void* q, const 
  *
  * The library writes s = max(amax / 448, 2^-100), amax the largest finite
  * magnitude of the block, and c = value / s rounded to nearest even; infinities
- * become +-448, NaN stays NaN.  The product takes any scales.
+ * become +-448, NaN stays NaN.  The product takes any scales whose products
+ * x_scales w_scales, which it forms first, are 0 or normal fp32 numbers: smaller
+ * ones lose digits, and what a larger one reaches is infinite or NaN.
  * ------------------------------------------------------------------------ */
 
 /* R rows of H heads of D channels. */
@@ -509,8 +511,19 @@ typedef struct gdr_matmul_dims {
  *     y[m,n] = bias[n] + sum_b x_scales[m,b] w_scales[n/128,b]
  *                                sum_{k in block b} x[m,k] w[n,k]
  *
- * over blocks b of 128 channels.  Each block's sum is fp32, and so is the sum
- * over blocks; y is rounded once.
+ * over blocks b of 128 channels.  The sum over blocks is fp32 and y is rounded
+ * once.  Within a block the output's type chooses the arithmetic:
+ *
+ *     fp32   products are exact and their sum is fp32
+ *     bf16   products are added 8 at a time, what lies 13 bits below the largest
+ *            of the 8 is dropped, and the groups' sums are added in fp32.  Next
+ *            to y's own rounding that is a hundredth for ordinary rows, but it can
+ *            reach 2^-10 of the sum of the terms' magnitudes, so that of a y that
+ *            its terms nearly cancel to no digit may be left.  Take fp32 for those
+ *
+ * The order in which blocks are added depends on the sizes and on the place of
+ * the row and column: the same call gives the same digits every time, equal rows
+ * at different places, or in calls of different sizes, may differ in their last.
  *
  *   dims      M rows, N outputs (within 2^31 - 257), K channels: a multiple of 16, up
  *             to 2^20
