@@ -685,7 +685,7 @@ def gdr_rope_freqs(R, base, *, kind=GDR_ROPE_NONE, factor=1.0, context=0.0, low=
     _TURNS or _INDEX) says how they are stretched to `factor` times `context`."""
     if not 2 <= R <= 512:
         raise ValueError(f"R = {R}: expected an even number from 2 to 512")
-    freq = torch.empty(R // 2, dtype=torch.float64)
+    freq = torch.empty(R // 2, dtype=torch.float64, device="cpu")
     magnitude = ctypes.c_float()
     s = gdr_rope_scaling(kind, factor, context, low, high)
     rc = (_lib or load_library()).gdr_rope_freqs(R, base, ctypes.byref(s), freq.data_ptr(),

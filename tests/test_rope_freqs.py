@@ -1,0 +1,20 @@
+"""Frequencies of the rotary positions on the host, whatever device tensors are made on."""
+from __future__ import annotations
+
+
+import torch
+
+import gated_delta_rule_40_amd as gdr
+
+
+def test_frequencies_are_on_the_cpu_whatever_the_default_device():
+    want, m = gdr.gdr_rope_freqs(64, 10000.0, kind=gdr.GDR_ROPE_LINEAR, factor=2.0)
+    with torch.device("meta"):
+        got, n = gdr.gdr_rope_freqs(64, 10000.0, kind=gdr.GDR_ROPE_LINEAR, factor=2.0)
+    assert got.device.type == "cpu" and n == m and torch.equal(got, want)
+    try:
+        torch.set_default_device("meta")
+        got, _ = gdr.gdr_rope_freqs(64, 10000.0)
+    finally:
+        torch.set_default_device(None)
+    assert got.device.type == "cpu" and got[0] == 1.0
