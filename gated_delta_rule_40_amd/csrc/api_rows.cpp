@@ -231,14 +231,17 @@ int gdr_rope_freqs(int32_t R, double base, const gdr_rope_scaling* scaling, doub
   if (s.kind != GDR_ROPE_NONE) {
     if (s.kind != GDR_ROPE_LINEAR && s.kind != GDR_ROPE_BASE && !ramp) return GDR_E_DTYPE;
     if (!isfinite(s.factor) || !(s.factor >= 1.0)) return GDR_E_UNSUPPORTED;
-    if (s.kind == GDR_ROPE_BASE && R == 2) return GDR_E_UNSUPPORTED;
+    if (s.kind == GDR_ROPE_BASE) {
+      if (R == 2) return GDR_E_UNSUPPORTED;
+      base *= pow(s.factor, static_cast<double>(R) / (R - 2));
+      if (!isfinite(base)) return GDR_E_UNSUPPORTED;
+    }
     if (ramp && (!isfinite(s.context) || !(s.context > 0.0) || !isfinite(s.high) ||
                  !(s.low > 0.0) || !(s.low < s.high)))
       return GDR_E_UNSUPPORTED;
   }
   if (!freq) return GDR_E_NULL;
   constexpr double kTwoPi = 6.283185307179586476925286766559;
-  if (s.kind == GDR_ROPE_BASE) base *= pow(s.factor, static_cast<double>(R) / (R - 2));
   // The index (as a real number) whose frequency makes `turns` turns over the context.
   auto index_of = [&](double turns) {
     return R * log(s.context / (turns * kTwoPi)) / (2.0 * log(base));

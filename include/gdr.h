@@ -611,7 +611,8 @@ typedef struct gdr_rope_scaling {
  *   R          even, 2 to 512
  *   base       finite and above 1
  *   scaling    NULL for none; factor >= 1; TURNS and INDEX: context > 0,
- *              0 < low < high; BASE: R > 2.  Else GDR_E_UNSUPPORTED
+ *              0 < low < high; BASE: R > 2, its larger base finite.  Else
+ *              GDR_E_UNSUPPORTED
  *   freq       [R/2] written; magnitude (may be NULL) written
  */
 int gdr_rope_freqs(int32_t R, double base, const gdr_rope_scaling* scaling, double* freq,
