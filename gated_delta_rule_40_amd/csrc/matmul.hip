@@ -93,26 +93,26 @@ __device__ __forceinline__ i32x8 join(i32x4 lo, i32x4 hi) {
 }
 
 // 16 bytes a lane from `base` (the same in every lane) + offset to LDS: lane l's go
-// to lds + 16 l.  Nothing waits for it here.  (m0, which takes the address in LDS, is
-// set by the compiler right before what needs it.  The wait states: one behind the write
-// of m0, five behind a vector instruction's of a scalar base.)
+// to lds + 16 l.  Nothing waits for it here.  The compiler writes m0, which
+// takes the address in LDS, and knows what it holds.  (The wait states: one behind that
+// write, five behind a vector instruction's of a scalar base.)
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, unsigned offset, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                :
-               : "s"(lds), "v"(offset), "s"(base)
+               : "{m0}"(lds), "v"(offset), "s"(base)
                : "memory");
 }
 __device__ __forceinline__ void load_to_lds(const uint8_t* p, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, off"
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, off"
                :
-               : "s"(lds), "v"(p)
+               : "{m0}"(lds), "v"(p)
                : "memory");
 }
 // 4 bytes a lane, lane l's to lds + 4 l.
 __device__ __forceinline__ void load_word_to_lds(const float* p, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, off"
+  asm volatile("s_nop 4\n\tglobal_load_lds_dword %1, off"
                :
-               : "s"(lds), "v"(p)
+               : "{m0}"(lds), "v"(p)
                : "memory");
 }
 __device__ __forceinline__ unsigned lds_address(const void* p) {
