@@ -599,7 +599,8 @@ def gdr_rms_norm(x, weight=None, y=None, codes=None, scales=None, *, residual=No
 
 def gdr_quant_rows(x, codes, scales, *, stream=None):
     """Rows x [R,K] (float32 or bfloat16; they may lie apart) to codes [R,K]
-    (float8_e4m3fn or uint8) and scales [R,ceil(K/128)] fp32."""
+    (float8_e4m3fn or uint8) and scales [R,ceil(K/128)] fp32.  K is a multiple of 128
+    or up to 32768."""
     if stream is None:
         rc = _quant_call(x, codes, scales)
         if rc is not None:
@@ -610,7 +611,8 @@ def gdr_quant_rows(x, codes, scales, *, stream=None):
     if codes is None:
         raise ValueError("codes is required")
     c, s = _f8_rows(codes, scales, R, W, dev)
-    # Any width: rows of whole blocks are heads of 128 channels side by side.
+    # Rows of whole blocks are heads of 128 channels side by side: any number of them.  Other
+    # rows are one head, of up to 32768 channels.
     H = W // 128 if W % 128 == 0 and W else 1
     _launch("gdr_quant_rows", dev, stream, _norm_dims(R, H, W // H), io, x.data_ptr(),
             _apart(x, "x", R, W), c, s)

@@ -17,9 +17,13 @@
 //
 // stream_kernel: few rows.  The weight is read once; the blocks of a row are shared by
 // the waves of a workgroup and their sums joined in LDS.  Bound by HBM (one row through
-// 8192 x 4096 7.8 us, 34 MB), and with the rows by the L2 caches that every workgroup
-// reads x from (64 rows 11.0 us; 64 x 1024 x 4096 5.8, K = 14336 12.0, in smaller tiles).
-// tile_kernel: many rows.  4000 rows through 8192 x 4096 129 us, 2.1 PFLOP/s; 8192^3 2.3.
+// 8192 x 4096 7.9 us, 34 MB), and with the rows by the L2 caches that every workgroup
+// reads x from (64 rows 11.2 us; 64 x 1000 x 4096 6.1, K = 14336 12.4, in smaller tiles).
+// tile_kernel: many rows.  4000 rows through 8192 x 4096 130 us, 2.1 PFLOP/s; 8192^3 2.3.
+// Between the two, 65 to 1000 rows, the one block under way is what bounds it: a step of a
+// workgroup waits for loads that began one step before (250 rows through 8192 x 4096 23 us,
+// 44 MB; 400 x 1000 12.2 us, 6 MB, with most CUs idle in large tiles and 80 MB loaded in
+// small ones, as workgroups share no sum over K).
 // The matrix pipes alone reach 3.5 on such codes, held by power (4.9 on zeros).  A step
 // of 2048 matrix cycles a SIMD takes about 3600: the loads into LDS cost some 400 of
 // the rest, reading operands 100, the barrier and what surrounds it most of it.
@@ -144,7 +148,10 @@ __device__ __forceinline__ void store_out(const MatmulArgs& a, int m, int n, f32
 }
 
 // Eight neighbouring outputs of row m from column n; `whole`: the columns are there, and
-// 16-byte aligned.
+// 16-byte aligned (where N is not of whole 16 bytes no output is: 4000 x 8191 x 4096 186 us,
+// 4000 x 8188 185, 4000 x 8192 132).  bf16 goes through the L2 caches at every size: 1000 x
+// 4096 x 1024 9.1 us against 10.2 with plain stores, 192 x 8192 x 4096 22.0 against 22.2, 1500
+// x 8192 x 4096 55.3 against 57.0.
 template <typename T>
 __device__ __forceinline__ void store_out8(const MatmulArgs& a, int m, int n, f32x4 lo, f32x4 hi,
                                            bool whole) {
@@ -233,8 +240,10 @@ __global__ __launch_bounds__(WAVES * 64) void stream_kernel(MatmulArgs a, int ro
   };
   // Rows a multiple of 4 KiB apart lie on the same memory channels: workgroups (32 at a time,
   // four of each XCD, which may share a weight's or x's rows) then begin at different blocks.
-  // 64 x 4096 x 4096 10.2 -> 8.5 us, 64 x 8192 12.1 -> 11.1, 1 x 8192 8.6 -> 7.8; other
-  // strides gain nothing (16 x 4096, K = 14336 11.5 and 12.1).
+  // 64 x 4096 x 4096 10.2 -> 8.5 us, 64 x 8192 12.1 -> 11.1, 1 x 8192 8.6 -> 7.8.  Rows an odd
+  // multiple of 2 KiB apart gain nothing (64 x 4096, K = 14336 19.3 and 19.8; 64 x 8192, K =
+  // 14336 39.5 and 39.9, K = 6144 13.9 and 13.8, K = 10240 21.1 and 26.3; 16 x 4096, K = 14336
+  // 11.1 and 11.2).
   const unsigned turn = K % 4096 == 0 ? blockIdx.x / 32 * WAVES : 0;
   const int first = blocks > 0 ? static_cast<int>(turn % blocks) : 0;
   auto block_of = [&](int t) { return t + first < blocks ? t + first : t + first - blocks; };
@@ -491,23 +500,25 @@ hipError_t launch_tile(const MatmulArgs& a, hipStream_t stream) {
 // ---------------------------------------------------------------------------
 // Which kernel.  Up to 16 rows a tile of as many; past that the one with the lowest
 // estimate, in microseconds, of a fixed cost and, for each round of 256 workgroups, one of
-// its own and one for 4096 channels of the rows that a workgroup loads (680 sizes from 20 x
+// its own and one for 4096 channels of the rows that a workgroup loads (704 sizes from 20 x
 // 512 to 1000 x 12288, K of 1024 to 14336, both output types: it takes 0.7% longer than the
-// fastest of them all on the average, more than 10% at 2% of them).  The tile_kernel is
+// fastest of them all on the average, more than 10% at 15 of them, and 38% at the worst, 400
+// x 4096, K = 8192: 58.5 us in 64 x 64, where the stream_kernel's time grows faster than K,
+// and 42.3 in the tile of 64 x 128; behind it come 17, 16 and 15%).  The tile_kernel is
 // left out up to 64 rows, where the weight is read once and HBM is what counts (17 x 65536
 // 57 us with 32 x 32, 70 with a tile of 64 x 128).  With few outputs smaller tiles reach
 // more CUs, each of which takes in some 68 bytes a ns:
-//   64 x 1024 stream 16 x 16 5.8 us, 32 x 16 5.6, 64 x 32 8.2; K = 14336 12.0, 12.6, 23.7
-//   128 x 1024 stream 16 x 16 8.3, 32 x 16 6.5, 32 x 32 7.2, 64 x 32 9.4
-//   64 x 4096 stream 32 x 16 9.5, 64 x 16 9.2, 64 x 32 10.1; K = 14336 25.7, 21.3, 24.8
-//   32 x 8192 stream 32 x 16 10.2, 32 x 32 10.0; 100 x 4096 64 x 16 14.4, 64 x 32 12.0
-//   64 x 8192 stream 64 x 32 12.2, stream 64 x 64 14.3; 64 x 16384 21.4, 16.7
-//   192 x 8192 stream 64 x 32 27.6, tile 64 x 128 24.6
-//   512 x 8192 tile 64 x 128 32.8, tile 128 x 128 31.8
-//   1000 x 8192 tile 128 x 128 49.1, tile 256 x 128 45.5
-//   1500 x 8192 tile 128 x 128 73.7, tile 256 x 256 62.6
+//   64 x 1000 stream 16 x 16 6.1 us, 32 x 16 6.4, 64 x 32 9.2; K = 14336 12.4, 13.3, 24.0
+//   128 x 1000 stream 16 x 16 8.5, 32 x 16 6.8, 32 x 32 7.6, 64 x 32 9.6
+//   64 x 4096 stream 32 x 32 8.7, 64 x 16 8.7, 64 x 32 10.1; K = 14336 20.5, 22.3, 25.9
+//   32 x 8192 stream 32 x 16 9.9, 32 x 32 8.7; 80 x 4096 64 x 16 14.4, 64 x 32 11.1
+//   64 x 8192 stream 64 x 32 11.4, stream 64 x 64 13.8; 64 x 12288 18.7, 15.3
+//   160 x 8192 stream 64 x 32 26.9, tile 64 x 128 23.0
+//   400 x 8192 tile 64 x 128 29.3, tile 128 x 128 28.9
+//   1000 x 8192 tile 128 x 128 43.8, tile 256 x 128 41.1
+//   1000 x 12288 tile 128 x 128 66.7, tile 256 x 256 58.1
 // An fp32 output's operands take twice the registers: the two that would not fit are left
-// out, and the tiles' products take longer (1000 x 8192: 73.4 and 68.3).
+// out, and the tiles' products take longer (1000 x 8192: 69.7 and 66.6).
 // ---------------------------------------------------------------------------
 enum class Plan {
   kStream16x16,

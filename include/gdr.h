@@ -439,8 +439,9 @@ int gdr_attn_cached(const gdr_kv_dims* dims, gdr_dtype io, const void* q, const 
  *     codes [R,K]    scales [R,ceil(K/128)]
  *
  * The library writes s = max(amax / 448, 2^-100), amax the largest finite
- * magnitude of the block, and c = value / s rounded to nearest even; infinities
- * become +-448, NaN stays NaN.  The product takes any scales whose products
+ * magnitude of the block, and c = value / s rounded to nearest even (each quotient
+ * a product with the fp32 reciprocal, first); infinities become +-448, NaN stays
+ * NaN.  The product takes any scales whose products
  * x_scales w_scales, which it forms first, are 0 or normal fp32 numbers: smaller
  * ones lose digits, and what a larger one reaches is infinite or NaN.
  * ------------------------------------------------------------------------ */
